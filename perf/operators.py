@@ -311,10 +311,11 @@ def _gathered(pool, table, kv, page):
 
 
 def _visible(n, kv, mask, device):
-    t = torch.arange(kv - n, kv, device=device)
+    """How many cached keys each new token sees: all, or those before the chunk and the chunk's blocks up to its own."""
     if mask == 0:
         return torch.full((n,), kv, device=device)
-    return ((torch.div(t, mask, rounding_mode="floor") + 1) * mask).clamp(0, kv)
+    t = torch.arange(n, device=device)
+    return (kv - n + (torch.div(t, mask, rounding_mode="floor") + 1) * mask).clamp(0, kv)
 
 
 def _scores(case, x):
@@ -402,7 +403,7 @@ def _pairs(case):
             total += n * kv
         else:
             m = case["mask"]
-            total += sum(max(0, min(kv, ((p // m) + 1) * m)) for p in range(kv - n, kv))
+            total += sum(max(0, min(kv, kv - n + (t // m + 1) * m)) for t in range(n))
     return total * case["heads"]
 
 
@@ -450,7 +451,7 @@ def _exact_rows(case, x, b, start, h):
     v = x["v_pool"][:, hk].reshape(-1, d)[at].double()
     logits = x["q"][start:start + n, h].double() @ k.T / math.sqrt(d)
     if case["mask"]:
-        block = torch.div(j, case["mask"], rounding_mode="floor")
+        block = torch.where(j < kv - n, -1, torch.div(j - (kv - n), case["mask"], rounding_mode="floor"))
         logits[block[None, :] > block[kv - n:, None]] = -math.inf
     return logits, v
 
