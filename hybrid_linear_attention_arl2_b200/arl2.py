@@ -25,6 +25,7 @@ STATUS = {
     3: "ARL2_ERR_OUT_OF_MEMORY", 4: "ARL2_ERR_CUDA", 5: "ARL2_ERR_TIMEOUT", 6: "ARL2_ERR_NO_DEVICE",
     7: "ARL2_ERR_SCRATCH_LIMIT",
     8: "ARL2_ERR_BOUNDS",
+    9: "ARL2_ERR_PAGE",
 }
 ARL2_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -43,7 +44,30 @@ class arl2_config(ctypes.Structure):
     ]
 
 
-_VP, _I32, _I64, _U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+class arl2_qk_prep(ctypes.Structure):
+    _fields_ = [
+        ("n_axes", ctypes.c_int32), ("axis_dim", ctypes.c_int32 * 3), ("halves", ctypes.c_int32),
+        ("theta", ctypes.c_float), ("eps", ctypes.c_float), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+    ]
+
+
+class arl2_paged_config(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class arl2_paged_batch(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+        ("max_kv", ctypes.c_int32), ("pages_ld", ctypes.c_int32),
+        ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+    ]
+
+
+_VP, _I32, _I64, _U64, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 _SIGS = {
     "arl2_state_init": (_I32, [ctypes.POINTER(arl2_config), _VP, _VP, _VP, _VP, ctypes.POINTER(_VP)]),
     "arl2_frame_query": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP]),
@@ -67,6 +91,16 @@ _SIGS = {
     "arl2_kv_device_bytes": (_I64, [_VP]),
     "arl2_kv_last_error": (_I32, [_VP]),
     "arl2_kv_destroy": (_I32, [_VP]),
+    "arl2_qk_norm_rope": (_I32, [_VP, _I32, _I32, _I32, _I32, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _I64, _VP]),
+    "arl2_paged_init": (_I32, [ctypes.POINTER(arl2_paged_config), _VP, _VP, _VP, ctypes.POINTER(_VP)]),
+    "arl2_paged_append": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP, _VP]),
+    "arl2_paged_attend": (_I32, [_VP, _VP, _VP, _I64, _I32, _VP, _VP, _VP]),
+    "arl2_paged_weights": (_I32, [_VP, _VP, _VP, _I64, _I32, _VP, _F32, _VP, _VP, _I64, _VP]),
+    "arl2_paged_evict": (_I32, [_VP, _VP, _VP, _I64, _I32, _I32, _I32, _VP, _I32, _VP, _VP, _VP, _VP]),
+    "arl2_paged_last_error": (_I32, [_VP]),
+    "arl2_paged_device_bytes": (_I64, [_VP]),
+    "arl2_paged_set_wait_limit": (_I32, [_VP, _U64]),
+    "arl2_paged_destroy": (_I32, [_VP]),
     "arl2_block_init": (_I32, [ctypes.POINTER(arl2_config), _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.POINTER(_VP)]),
     "arl2_block_query": (_I32, [_VP, _VP, _VP, _VP]),
     "arl2_block_commit": (_I32, [_VP, _VP, _VP, _VP]),
@@ -239,6 +273,63 @@ def arl2_kv_commit_strided(h, q, k, v, ld, o, stream=None) -> None:
 
 def arl2_kv_destroy(h) -> None:
     _check(load_library().arl2_kv_destroy(h), "arl2_kv_destroy")
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def arl2_qk_norm_rope(prep: arl2_qk_prep, dtype, heads, kv_heads, head_dim, tokens, q, k, ld, pos, q_out, k_out,
+                      ld_out, stream=None) -> None:
+    _check(load_library().arl2_qk_norm_rope(_ref(prep), dtype, heads, kv_heads, head_dim, tokens, _ptr(q), _ptr(k), ld,
+                                            _ptr(pos), _ptr(q_out), _ptr(k_out), ld_out, _stream(stream)),
+           "arl2_qk_norm_rope")
+
+
+def arl2_paged_init(cfg: arl2_paged_config, k_pool, v_pool, stream=None) -> int:
+    h = _VP()
+    _check(load_library().arl2_paged_init(ctypes.byref(cfg), _ptr(k_pool), _ptr(v_pool), _stream(stream),
+                                          ctypes.byref(h)), "arl2_paged_init")
+    return h.value
+
+
+def arl2_paged_append(h, batch: arl2_paged_batch, prep, q, k, v, ld, pos, q_out, stream=None) -> None:
+    _check(load_library().arl2_paged_append(h, _ref(batch), _ref(prep), _ptr(q), _ptr(k), _ptr(v), ld, _ptr(pos),
+                                            _ptr(q_out), _stream(stream)), "arl2_paged_append")
+
+
+def arl2_paged_attend(h, batch: arl2_paged_batch, q, ld_q, mask_block, o, lse, stream=None) -> None:
+    _check(load_library().arl2_paged_attend(h, _ref(batch), _ptr(q), ld_q, mask_block, _ptr(o), _ptr(lse),
+                                            _stream(stream)), "arl2_paged_attend")
+
+
+def arl2_paged_weights(h, batch: arl2_paged_batch, q, ld_q, mask_block, lse, decay, w_in, w_out, w_ld,
+                       stream=None) -> None:
+    _check(load_library().arl2_paged_weights(h, _ref(batch), _ptr(q), ld_q, mask_block, _ptr(lse), decay, _ptr(w_in),
+                                             _ptr(w_out), w_ld, _stream(stream)), "arl2_paged_weights")
+
+
+def arl2_paged_evict(h, batch: arl2_paged_batch, w_in, w_ld, budget, sink, recent, dst_pages, dst_ld, w_out, kept,
+                     kv_len_out, stream=None) -> None:
+    _check(load_library().arl2_paged_evict(h, _ref(batch), _ptr(w_in), w_ld, budget, sink, recent, _ptr(dst_pages),
+                                           dst_ld, _ptr(w_out), _ptr(kept), _ptr(kv_len_out), _stream(stream)),
+           "arl2_paged_evict")
+
+
+def arl2_paged_last_error(h) -> int:
+    return load_library().arl2_paged_last_error(h)
+
+
+def arl2_paged_device_bytes(h) -> int:
+    return load_library().arl2_paged_device_bytes(h)
+
+
+def arl2_paged_set_wait_limit(h, limit_ns: int) -> None:
+    _check(load_library().arl2_paged_set_wait_limit(h, limit_ns), "arl2_paged_set_wait_limit")
+
+
+def arl2_paged_destroy(h) -> None:
+    _check(load_library().arl2_paged_destroy(h), "arl2_paged_destroy")
 
 
 def arl2_block_init(cfg: arl2_config, w_qkv, w_o, w_gate, phi_q, phi_k, phi_v, stream=None) -> int:
@@ -433,6 +524,249 @@ class KVLayer:
     def close(self):
         if self.handle:
             arl2_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _token_rows(heads, d, dtype, device, **tensors):
+    """The common pitch of [tokens, heads, head_dim] views in elements (0: each
+    contiguous), and their tokens; raises where the library cannot read them."""
+    ld = tokens = None
+    dense = True
+    for name, t in tensors.items():
+        h = heads[name]
+        if t.dim() != 3 or t.shape[1] != h or t.shape[2] != d or t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name}: expected [tokens, {h}, {d}] of {dtype} on {device}, "
+                             f"got {list(t.shape)} of {t.dtype} on {t.device}")
+        if tokens is None:
+            tokens = t.shape[0]
+        elif t.shape[0] != tokens:
+            raise ValueError(f"{name}: {t.shape[0]} tokens, expected {tokens}")
+        s = t.stride()
+        if s[2] != 1 or (h > 1 and s[1] != d):
+            raise ValueError(f"{name}: a token's row must be contiguous")
+        if tokens > 1:
+            dense = dense and s[0] == h * d
+            if ld is None:
+                ld = s[0]
+            elif ld != s[0]:
+                ld = -1
+    if dense:
+        return 0, tokens
+    if ld < 0:
+        raise ValueError("strided views must have one pitch")
+    return ld, tokens
+
+
+def _plain(name, t, dtype, device, shape=None):
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor{'' if shape is None else f' {list(shape)}'} on "
+                         f"{device}, got {list(t.shape)} of {t.dtype} on {t.device}")
+    return t
+
+
+def _stream_of(device, stream):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+class QKPrep:
+    """Norm and rotation of queries and keys: norm weights (None, None: no
+    norm) and up to three position axes."""
+
+    def __init__(self, axis_dims, theta=10000.0, halves=False, eps=1e-6, w_q=None, w_k=None):
+        axis_dims = list(axis_dims)
+        if len(axis_dims) > 3:
+            raise ValueError("at most three axes")
+        if (w_q is None) != (w_k is None):
+            raise ValueError("norm weights come in pairs")
+        for name, w in (("w_q", w_q), ("w_k", w_k)):
+            if w is not None and (w.dim() != 1 or not w.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous [head_dim]")
+        self.w_q, self.w_k, self.n_axes = w_q, w_k, len(axis_dims)
+        self.struct = arl2_qk_prep(len(axis_dims), (ctypes.c_int32 * 3)(*axis_dims), int(halves), theta, eps,
+                                   _ptr(w_q), _ptr(w_k))
+
+    def _check(self, d, dtype, device, tokens, pos):
+        import torch
+        for name, w in (("w_q", self.w_q), ("w_k", self.w_k)):
+            if w is not None:
+                _plain(name, w, dtype, device, (d,))
+        if self.n_axes:
+            if pos is None:
+                raise ValueError("pos: the prep's axes need positions")
+            _plain("pos", pos, torch.int32, device, (tokens, self.n_axes))
+
+
+def qk_norm_rope(prep: QKPrep, q, k, pos=None, q_out=None, k_out=None, stream=None):
+    """Norm and rotate queries [tokens, heads, d] and keys [tokens, kv_heads, d]
+    (views of one pitch, or contiguous) in one pass; returns (q_out, k_out)."""
+    import torch
+    d, dev = q.shape[2], q.device
+    heads = {"q": q.shape[1], "k": k.shape[1]}
+    ld, tokens = _token_rows(heads, d, q.dtype, dev, q=q, k=k)
+    prep._check(d, q.dtype, dev, tokens, pos)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
+    ld_out, n = _token_rows(heads, d, q.dtype, dev, q=q_out, k=k_out)
+    if n != tokens:
+        raise ValueError("outputs: as many tokens as the inputs")
+    with torch.cuda.device(dev):
+        arl2_qk_norm_rope(prep.struct, _abi_dtype(q.dtype), heads["q"], heads["k"], d, tokens, q, k, ld,
+                          pos if prep.n_axes else None, q_out, k_out, ld_out, _stream_of(dev, stream))
+    return q_out, k_out
+
+
+def _abi_dtype(dtype):
+    import torch
+    if dtype == torch.bfloat16:
+        return ARL2_BF16
+    if dtype == torch.float32:
+        return ARL2_F32
+    raise ValueError(f"float32 or bfloat16 tensors, got {dtype}")
+
+
+class PagedBatch:
+    """The streams of one call: q_start int32 [n + 1], kv_len int32 [n], pages
+    int32 [n, pages_ld] on the device, and the host's bounds of their values.
+    The tensors may be rewritten between calls (and between replays of a graph)."""
+
+    def __init__(self, q_start, kv_len, pages, *, tokens, max_q, max_kv):
+        import torch
+        n = kv_len.shape[0]
+        if pages.dim() != 2 or pages.shape[0] != n:
+            raise ValueError("pages: expected [streams, pages]")
+        _plain("kv_len", kv_len, torch.int32, kv_len.device, (n,))
+        _plain("q_start", q_start, torch.int32, kv_len.device, (n + 1,))
+        _plain("pages", pages, torch.int32, kv_len.device)
+        self.q_start, self.kv_len, self.pages = q_start, kv_len, pages
+        self.tokens, self.device = tokens, kv_len.device
+        self.struct = arl2_paged_batch(n, tokens, max_q, max_kv, pages.shape[1], _ptr(q_start), _ptr(kv_len),
+                                       _ptr(pages))
+
+
+class PagedKVLayer:
+    """A softmax layer on a paged KV cache (a handle of the C ABI).  The pools
+    are [n_pages, kv_heads, page_size, head_dim]; the layer keeps them alive."""
+
+    def __init__(self, heads, kv_heads, head_dim, dtype, k_pool, v_pool, *, softmax_scale=0.0, stream=None):
+        import torch
+        self.handle = None
+        self.dtype, self.device = _torch_dtype(dtype), k_pool.device
+        if k_pool.dim() != 4 or k_pool.shape[1] != kv_heads or k_pool.shape[3] != head_dim:
+            raise ValueError("k_pool: expected [n_pages, kv_heads, page_size, head_dim]")
+        _plain("k_pool", k_pool, self.dtype, self.device)
+        _plain("v_pool", v_pool, self.dtype, self.device, k_pool.shape)
+        self.k_pool, self.v_pool = k_pool, v_pool
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.cfg = arl2_paged_config(heads, kv_heads, head_dim, k_pool.shape[2], k_pool.shape[0], dtype, softmax_scale)
+        with torch.cuda.device(self.device):
+            self.handle = arl2_paged_init(self.cfg, k_pool, v_pool, _stream_of(self.device, stream))
+
+    def _batch(self, batch):
+        if batch.device != self.device:
+            raise ValueError(f"batch on {batch.device}, layer on {self.device}")
+        return batch.struct
+
+    def _rows(self, batch, **tensors):
+        heads = {"q": self.heads, "q_out": self.heads, "k": self.kv_heads, "v": self.kv_heads, "o": self.heads}
+        ld, tokens = _token_rows(heads, self.head_dim, self.dtype, self.device, **tensors)
+        if tokens != batch.tokens:
+            raise ValueError(f"{tokens} token rows, the batch has {batch.tokens}")
+        return ld
+
+    def append(self, batch, k, v, *, q=None, prep=None, pos=None, q_out=None, stream=None):
+        """Store the new tokens' K and V; with a prep, K normed and rotated, and
+        q's turned rows are returned (q_out)."""
+        import torch
+        st = self._batch(batch)
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            ld = self._rows(batch, k=k, v=v)
+        else:
+            if prep is None:
+                raise ValueError("q without a prep")
+            ld = self._rows(batch, q=q, k=k, v=v)
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+            if self._rows(batch, q_out=q_out):
+                raise ValueError("q_out must be contiguous")
+        if prep is not None:
+            prep._check(self.head_dim, self.dtype, self.device, batch.tokens, pos)
+        arl2_paged_append(self.handle, st, None if prep is None else prep.struct, q, k, v, ld,
+                          pos if prep is not None and prep.n_axes else None, q_out, _stream_of(self.device, stream))
+        return q_out
+
+    def attend(self, batch, q, *, mask_block=0, o=None, lse=None, stream=None):
+        """(O, lse) of the new tokens over their streams' cached keys."""
+        import torch
+        st = self._batch(batch)
+        ld = self._rows(batch, q=q)
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+        if self._rows(batch, o=o):
+            raise ValueError("o must be contiguous")
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        else:
+            _plain("lse", lse, torch.float32, self.device, q.shape[:2])
+        arl2_paged_attend(self.handle, st, q, ld, mask_block, o, lse, _stream_of(self.device, stream))
+        return o, lse
+
+    def _weights_shape(self, batch, w):
+        import torch
+        if w.dim() != 3 or w.shape[0] != batch.struct.n_seqs or w.shape[1] != self.kv_heads:
+            raise ValueError(f"w: expected [{batch.struct.n_seqs}, {self.kv_heads}, keys], got {list(w.shape)}")
+        _plain("w", w, torch.float32, self.device)
+
+    def weights(self, batch, q, lse, w, *, mask_block=0, decay=1.0, w_out=None, stream=None):
+        """The cached keys' accumulated attention weights after the new tokens
+        (w_out may be w)."""
+        import torch
+        st = self._batch(batch)
+        ld = self._rows(batch, q=q)
+        self._weights_shape(batch, w)
+        _plain("lse", lse, torch.float32, self.device, q.shape[:2])
+        if w_out is None:
+            w_out = torch.empty_like(w)
+        else:
+            _plain("w_out", w_out, torch.float32, self.device, w.shape)
+        arl2_paged_weights(self.handle, st, q, ld, mask_block, lse, decay, w, w_out, w.shape[2],
+                           _stream_of(self.device, stream))
+        return w_out
+
+    def evict(self, batch, w, dst_pages, *, budget, sink=0, recent=0, stream=None):
+        """Cut the streams to at most `budget` keys, moved to dst_pages; returns
+        (kv_len, w, kept) of the streams in their new pages."""
+        import torch
+        st = self._batch(batch)
+        self._weights_shape(batch, w)
+        n = batch.struct.n_seqs
+        if dst_pages.dim() != 2 or dst_pages.shape[0] != n:
+            raise ValueError("dst_pages: expected [streams, pages]")
+        _plain("dst_pages", dst_pages, torch.int32, self.device)
+        w_out = torch.empty_like(w)
+        kept = torch.empty((n, self.kv_heads, budget), dtype=torch.int32, device=self.device)
+        kv_len = torch.empty((n,), dtype=torch.int32, device=self.device)
+        arl2_paged_evict(self.handle, st, w, w.shape[2], budget, sink, recent, dst_pages, dst_pages.shape[1], w_out,
+                         kept, kv_len, _stream_of(self.device, stream))
+        return kv_len, w_out, kept
+
+    def last_error(self) -> int:
+        return arl2_paged_last_error(self.handle)
+
+    def device_bytes(self) -> int:
+        return arl2_paged_device_bytes(self.handle)
+
+    def close(self):
+        if self.handle:
+            arl2_paged_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

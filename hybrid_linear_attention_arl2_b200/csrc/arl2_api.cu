@@ -135,6 +135,12 @@ float softmax_scale(const arl2_config& c) {
 
 }  // namespace
 
+namespace arl2 {
+cudaError_t device_alloc(void** p, size_t bytes) { return dev_alloc(p, bytes); }
+arl2_status status_of_cuda(cudaError_t e) { return from_cuda(e); }
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+}  // namespace arl2
+
 struct arl2_state {
   uint64_t magic;
   arl2_config cfg;
@@ -316,6 +322,7 @@ const char* arl2_status_string(arl2_status s) {
     case ARL2_ERR_NO_DEVICE: return "no CUDA device";
     case ARL2_ERR_SCRATCH_LIMIT: return "sizes exceed the fixed scratch of the allocation-free state write";
     case ARL2_ERR_BOUNDS: return "a kernel index check failed (debug build)";
+    case ARL2_ERR_PAGE: return "a page, length or offset in device memory is out of range";
   }
   return "unknown status";
 }

@@ -30,6 +30,13 @@ uint64_t layer_wait_limit(::arl2_state* h);
 arl2_status token_pass(::arl2_state* h, const void* q, const void* k, const void* v, const float* alpha_tok,
                        const float* beta, void* o, cudaStream_t st, bool commit);
 
+// What other translation units share of arl2_api.cu's host code: device
+// allocation (counted by the allocation failure injection), the status of a
+// CUDA error, and the driver's tensor-map encoder (null without a driver).
+cudaError_t device_alloc(void** p, size_t bytes);
+arl2_status status_of_cuda(cudaError_t e);
+void* tensor_map_encoder();
+
 // Token-level pass (token_level.cu): operands, scratch and launch.  Q, K, V,
 // O bf16 [B, L, H, 128] contiguous (O holds the intra-frame output on entry);
 // phi_q [H][i][j] as given, phi_k and phi_v transposed ([H][j][i]); alpha_tok

@@ -1,0 +1,411 @@
+// Paged KV cache on CUDA cores (float32 tensors): attention of new tokens over
+// the pages, the weights the cached keys received, and the kernel that joins
+// the pieces of items cut by the CTAs' ranges (both types).
+//
+//   O = softmax(Q K^T scale) V over the visible keys,  lse = log sum exp,
+//   w_out[j] = decay w_in[j] + sum over rows of exp(s_j - lse)
+//
+// One pass over the keys with the running maximum and sum of each row (Q K^T
+// in units of log2).  A CTA holds 64 query rows (token, head of the group) of
+// one key head and takes tiles of 64 keys; S and O are 4 x 4 and 4 x d/16
+// register tiles a thread, P passes through shared memory.  The f32 path is
+// bound by the FMA pipe: 4 d FMAs a (row, key) pair.
+
+#include <cuda_bf16.h>
+
+#include "paged.h"
+#include "params.h"
+#include "sm100.cuh"
+
+namespace arl2 {
+
+namespace {
+
+constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+using Plan = PagedPlan<1, kRows, kKeys>;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// Rows of keys [k0, k0 + 64) of stream b and head hk into dst[64][ld] as
+// float; keys at or past `end` and keys of pages that are none read as zeros.
+template <typename T>
+__device__ __forceinline__ void load_keys(float* dst, int ld, const T* pool, const PagedSeqs& s, int b, int hk,
+                                          int kv_heads, int d, int k0, int end, uint32_t* err) {
+  const int v4 = d >> 2;
+  for (int i = threadIdx.x; i < kKeys * v4; i += kThreads) {
+    const int r = i / v4, c = (i - r * v4) * 4, j = k0 + r;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < end) {
+      const int pg = page_of(s, b, j, err);
+      if (pg >= 0) v = load4(pool + ((int64_t(pg) * kv_heads + hk) * s.page_size + j % s.page_size) * d + c);
+    }
+    store4(dst + r * ld + c, v);
+  }
+}
+
+// S = Q K^T for this thread's 4 rows (4 ty ..) x 4 keys (tx + 16 i).
+__device__ __forceinline__ void scores(const float* sQ, const float* sK, int ld, int d, int ty, int tx,
+                                       float (&acc)[4][4]) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[a][i] = 0.f;
+  for (int c = 0; c < d; c += 4) {
+    float4 q[4], k[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) q[a] = *reinterpret_cast<const float4*>(sQ + (4 * ty + a) * ld + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sK + (tx + 16 * i) * ld + c);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[a][i] = dot4(q[a], k[i], acc[a][i]);
+  }
+}
+
+__host__ __device__ inline size_t smem_floats(int d) {
+  return size_t(2 * kRows + kKeys) * (d + 4) + size_t(kKeys) * (kRows + 4);
+}
+
+// DC: 64-column chunks of the head dimension a thread accumulates (d <= 64 DC).
+template <typename T, int DC>
+__global__ void __launch_bounds__(kThreads)
+paged_attn_kernel(const PagedAttnParams p) {
+  extern __shared__ float sm[];
+  __shared__ long long sh[64];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
+  float* sQ = sm;
+  float* sK = sQ + kRows * ld;
+  float* sV = sK + kKeys * ld;
+  float* sP = sV + kKeys * ld;  // [key][row], pitch 68
+  constexpr int kPl = kRows + 4;
+  const PagedRange range = paged_range<Plan, kThreads>(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block, blockIdx.x,
+                                                       gridDim.x, p.err, sh);
+  if (tid < 2) p.rec[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
+  __syncthreads();
+  const T* q = static_cast<const T*>(p.q);
+  PagedWalk<Plan> walk(range, p.n_qblk);
+  while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
+    const PagedSeg<Plan>& s = walk.seg;
+    const int rows = s.blk.n_tok * p.group;
+    // query rows, and each of this thread's rows' visible keys
+    for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
+      const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows)
+        v = load4(q + int64_t(s.blk.q0 + s.blk.t0 + r / p.group) * p.ld_q + (s.hk * p.group + r % p.group) * d + c);
+      store4(sQ + r * ld + c, v);
+    }
+    int lim[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = 4 * ty + a;
+      lim[a] = r < rows ? visible_keys(s.blk.v, p.mask_block, s.blk.t0 + r / p.group) : 0;
+    }
+    float m[4], l[4], o[4][4 * DC];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      m[a] = -INFINITY;
+      l[a] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4 * DC; ++c) o[a][c] = 0.f;
+    }
+    for (int j = s.u0; j < s.u1; ++j) {
+      const int k0 = j * kKeys;
+      __syncthreads();
+      load_keys(sK, ld, static_cast<const T*>(p.k_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
+      load_keys(sV, ld, static_cast<const T*>(p.v_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
+      __syncthreads();
+      float acc[4][4];
+      scores(sQ, sK, ld, d, ty, tx, acc);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[a][i] = k0 + tx + 16 * i < lim[a] ? acc[a][i] * p.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, acc[a][i]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float mn = fmaxf(m[a], mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: every exponential is 0
+        const float corr = exp2f(m[a] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[a][i] = exp2f(acc[a][i] - ref);
+          sum += acc[a][i];
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l[a] = fmaf(l[a], corr, sum);
+        m[a] = mn;
+#pragma unroll
+        for (int c = 0; c < 4 * DC; ++c) o[a][c] *= corr;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(sP + (tx + 16 * i) * kPl + 4 * ty) =
+            make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
+      __syncthreads();
+#pragma unroll 4
+      for (int k = 0; k < kKeys; ++k) {
+        const float4 pk = *reinterpret_cast<const float4*>(sP + k * kPl + 4 * ty);
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const int col = tx * 4 + 64 * c;
+          if (col < d) {
+            const float4 v = *reinterpret_cast<const float4*>(sV + k * ld + col);
+            const float pr[4] = {pk.x, pk.y, pk.z, pk.w};
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              o[a][4 * c] = fmaf(pr[a], v.x, o[a][4 * c]);
+              o[a][4 * c + 1] = fmaf(pr[a], v.y, o[a][4 * c + 1]);
+              o[a][4 * c + 2] = fmaf(pr[a], v.z, o[a][4 * c + 2]);
+              o[a][4 * c + 3] = fmaf(pr[a], v.w, o[a][4 * c + 3]);
+            }
+          }
+        }
+      }
+    }
+    const bool whole = s.whole();
+    const int piece = 2 * blockIdx.x + s.slot();
+    if (!whole && tid == 0) p.rec[piece] = make_int4(s.f, s.hk, s.starts(), s.ends());
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = 4 * ty + a;
+      if (r >= rows) continue;
+      const int64_t orow = int64_t(s.blk.q0 + s.blk.t0 + r / p.group) * p.heads + s.hk * p.group + r % p.group;
+      const float inv = !whole ? 1.f : l[a] > 0.f ? 1.f / l[a] : 0.f;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const int col = tx * 4 + 64 * c;
+        if (col >= d) continue;
+        const float4 x = make_float4(o[a][4 * c] * inv, o[a][4 * c + 1] * inv, o[a][4 * c + 2] * inv,
+                                     o[a][4 * c + 3] * inv);
+        if (whole)
+          store4(static_cast<T*>(p.o) + orow * d + col, x);
+        else
+          store4(p.part_o + (int64_t(piece) * kRows + r) * d + col, x);
+      }
+      if (tx == 0) {
+        if (!whole)
+          p.part_ml[int64_t(piece) * kRows + r] = make_float2(m[a], l[a]);
+        else if (p.lse)
+          p.lse[orow] = l[a] > 0.f ? (m[a] + log2f(l[a])) * 0.69314718055994531f : -INFINITY;
+      }
+    }
+    __syncthreads();  // sQ is read no more
+  }
+}
+
+// ------------------------------------------------------------------ weights
+// One CTA per (stream, key head, 64 keys): every new token's rows go past in
+// tiles of 64, a thread sums its 4 rows' weights of its 4 keys.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+paged_weights_kernel(const PagedWeightParams p, int n_kt) {
+  extern __shared__ float sm[];
+  __shared__ float part[16][kKeys];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
+  float* sQ = sm;
+  float* sK = sQ + kRows * ld;
+  const T* q = static_cast<const T*>(p.q);
+  const int qt = kRows / p.group;
+  const long long items = (long long)p.s.n_seqs * p.kv_heads * n_kt;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int jt = int(it % n_kt), hk = int(it / n_kt % p.kv_heads), b = int(it / n_kt / p.kv_heads);
+    const SeqView v = load_seq(p.s, b, p.err);
+    const int k0 = jt * kKeys;
+    if (v.n < 0) continue;
+    float* out = p.w_out + (int64_t(b) * p.kv_heads + hk) * p.w_ld;
+    const float* in = p.w_in + (int64_t(b) * p.kv_heads + hk) * p.w_ld;
+    if (k0 < v.kv) {
+      __syncthreads();
+      load_keys(sK, ld, static_cast<const T*>(p.k_pool), p.s, b, hk, p.kv_heads, d, k0, v.kv, p.err);
+      float w[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t0 = 0; t0 < v.n; t0 += qt) {
+        const int rows = min(qt, v.n - t0) * p.group;
+        if (visible_keys(v, p.mask_block, min(t0 + qt, v.n) - 1) <= k0) continue;  // no row of the tile sees the keys
+        __syncthreads();
+        for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
+          const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < rows) x = load4(q + int64_t(v.q0 + t0 + r / p.group) * p.ld_q + (hk * p.group + r % p.group) * d + c);
+          store4(sQ + r * ld + c, x);
+        }
+        __syncthreads();
+        float acc[4][4];
+        scores(sQ, sK, ld, d, ty, tx, acc);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int r = 4 * ty + a;
+          if (r >= rows) continue;
+          const int t = t0 + r / p.group, lim = visible_keys(v, p.mask_block, t);
+          const float lse = p.lse[int64_t(v.q0 + t) * p.heads + hk * p.group + r % p.group];
+          if (lse == -INFINITY) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (k0 + tx + 16 * i < lim) w[i] += exp2f(fmaf(acc[a][i], p.scale_log2, -1.4426950408889634f * lse));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[ty][tx + 16 * i] = w[i];
+      __syncthreads();
+      if (tid < kKeys && k0 + tid < v.kv) {
+        float sum = 0.f;
+        for (int y = 0; y < 16; ++y) sum += part[y][tid];
+        out[k0 + tid] = fmaf(p.decay, in[k0 + tid], sum);
+      }
+      __syncthreads();
+    }
+    if (tid < kKeys && k0 + tid >= v.kv && k0 + tid < p.w_ld) out[k0 + tid] = 0.f;
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// The pieces of an item that several CTAs share, in key order: with M the
+// largest of their maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  The
+// CTA whose range the item starts in owns it (at most one per CTA); its
+// continuations are the next CTAs' slots 0.  A warp per row; reads are the
+// pieces, just written, from L2.
+constexpr int kCombineRows = 32;
+
+template <typename T, class P, int kPieceRows, int kTileRows>
+__global__ void __launch_bounds__(256)
+paged_combine_kernel(const PagedAttnParams p, int ctas) {
+  grid_dependency_wait();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int slot = -1;
+  int4 rec = p.rec[2 * c];
+  if (rec.x >= 0 && rec.z && !rec.w) slot = 0;
+  if (slot < 0) {
+    rec = p.rec[2 * c + 1];
+    if (rec.x >= 0 && rec.z && !rec.w) slot = 1;
+  }
+  if (slot < 0) return;
+  int n = 1;  // pieces: this one, then slots 0 of the CTAs after it up to the one that ends the item
+  for (int base = c + 1; base < ctas; base += 32) {
+    const bool end = base + lane < ctas && p.rec[2 * (base + lane)].w != 0;
+    const unsigned b = __ballot_sync(0xffffffffu, end);
+    if (b) {
+      n = base - c + __ffs(b);
+      break;
+    }
+  }
+  const int f = rec.x, hk = rec.y;
+  const typename P::Block blk = P::block(p.s, f / p.n_qblk, f % p.n_qblk, p.group, p.mask_block, nullptr);
+  const int qt = P::tile_tokens(p.group);
+  for (int i = warp; i < kCombineRows; i += 8) {
+    const int r = blockIdx.y * kCombineRows + i;
+    const int tile = r / kTileRows, rr = r % kTileRows, tt = tile * qt + rr / p.group;
+    if (r >= kPieceRows || rr >= qt * p.group || tt >= blk.n_tok) continue;
+    auto piece = [&](int k) { return int64_t(k == 0 ? 2 * c + slot : 2 * (c + k)) * kPieceRows + r; };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[piece(k)].x);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float2 ml = p.part_ml[piece(k)];
+        const float w = exp2f(ml.x - M);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane * 4 < p.d) v = load4(p.part_o + piece(k) * p.d + lane * 4);
+        L = fmaf(ml.y, w, L);
+        acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int64_t orow = int64_t(blk.q0 + blk.t0 + tt) * p.heads + hk * p.group + rr % p.group;
+    if (lane * 4 < p.d)
+      store4(static_cast<T*>(p.o) + orow * p.d + lane * 4,
+             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <typename T, int kTiles, int kTileRows, int kKeysOf>
+cudaError_t launch_combine(const PagedAttnParams& p, int grid, cudaStream_t st) {
+  constexpr int kPiece = kTiles * kTileRows;
+  // rows of a piece: the streams' own where they fit one tile
+  const int rows = p.s.max_q <= kTileRows / p.group ? p.s.max_q * p.group : kPiece;
+  const int y = (rows + kCombineRows - 1) / kCombineRows;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(grid), unsigned(y < 1 ? 1 : y));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, PagedPlan<kTiles, kTileRows, kKeysOf>, kPiece, kTileRows>, p,
+                            grid);
+}
+
+template <typename T, int DC>
+cudaError_t launch_attn(PagedAttnParams p, int grid, cudaStream_t st) {
+  static unsigned done = 0;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_kernel<T, DC>),
+                                   int(smem_floats(128) * sizeof(float)), &done);
+  if (e != cudaSuccess) return e;
+  const int qt = kRows / p.group;
+  p.n_qblk = (p.s.max_q + qt - 1) / qt;
+  if ((long long)p.n_qblk * p.s.n_seqs >= (1LL << 31)) return cudaErrorInvalidValue;
+  paged_attn_kernel<T, DC><<<grid, kThreads, smem_floats(p.d) * sizeof(float), st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_combine<T, 1, kRows, kKeys>(p, grid, st);
+}
+
+template <typename T>
+cudaError_t launch_weights(const PagedWeightParams& p, cudaStream_t st) {
+  const int bytes = int(size_t(kRows + kKeys) * (p.d + 4) * sizeof(float));
+  static unsigned done = 0;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_kernel<T>),
+                                   int(size_t(kRows + kKeys) * 132 * sizeof(float)), &done);
+  if (e != cudaSuccess) return e;
+  const long long n_kt = (p.w_ld + kKeys - 1) / kKeys;
+  const long long items = n_kt * p.s.n_seqs * p.kv_heads;
+  const unsigned grid = unsigned(items < (1 << 20) ? items : (1 << 20));
+  paged_weights_kernel<T><<<grid, kThreads, bytes, st>>>(p, int(n_kt));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// (two blocks to an SM with head dims up to 64)
+int paged_attn_grid(int, int sms) { return 2 * sms; }
+int paged_piece_rows(int) { return kRows; }
+
+cudaError_t launch_paged_attn(PagedAttnParams p, int dtype, int grid, cudaStream_t st) {
+  if (dtype == ARL2_BF16) return launch_attn<__nv_bfloat16, 2>(p, grid, st);
+  return p.d <= 64 ? launch_attn<float, 1>(p, grid, st) : launch_attn<float, 2>(p, grid, st);
+}
+
+cudaError_t launch_paged_weights(const PagedWeightParams& p, int dtype, int, cudaStream_t st) {
+  return dtype == ARL2_BF16 ? launch_weights<__nv_bfloat16>(p, st) : launch_weights<float>(p, st);
+}
+
+}  // namespace arl2

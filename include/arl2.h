@@ -65,9 +65,12 @@ typedef enum {
   ARL2_ERR_NO_DEVICE = 6,        /* no usable CUDA device / driver */
   ARL2_ERR_SCRATCH_LIMIT = 7,    /* sizes need more than the fixed scratch of
                                     arl2_state_write_noalloc */
-  ARL2_ERR_BOUNDS = 8            /* debug builds (libarl2_debug.so) only: a
+  ARL2_ERR_BOUNDS = 8,           /* debug builds (libarl2_debug.so) only: a
                                     kernel's index check failed and the access
                                     was skipped; surfaced by arl2_last_error */
+  ARL2_ERR_PAGE = 9              /* paged cache: a page number, length or offset
+                                    that a kernel read from device memory is out
+                                    of range; surfaced by arl2_paged_last_error */
 } arl2_status;
 
 typedef enum { ARL2_F32 = 0, ARL2_BF16 = 1 } arl2_dtype;
@@ -199,6 +202,172 @@ int64_t arl2_kv_frames(arl2_kv_t kv);
 int64_t arl2_kv_device_bytes(arl2_kv_t kv);
 arl2_status arl2_kv_last_error(arl2_kv_t kv);
 arl2_status arl2_kv_destroy(arl2_kv_t kv);
+
+/* ---- Norm and rotation of queries and keys ---------------------------------
+ * What a DiT or language-model block does to Q and K between its projection
+ * and its attention, in one pass: per token and head
+ *   y = x * rsqrt(mean(x^2) + eps) * w                     (over head_dim)
+ * and then the rotation of pairs of channels by the token's position:
+ *   (y0, y1) -> (y0 cos a - y1 sin a, y0 sin a + y1 cos a),
+ *   a = pos[token][axis] * theta^(-2 i / axis_dim[axis]).
+ * The axes take their axis_dim / 2 pairs one after the other (1 axis: a text
+ * or frame position; 3 axes: frame, row and column of a video token); i counts
+ * within the axis.  Pair p is channels (2p, 2p + 1), or with halves = 1
+ * channels (p, p + R/2), R = sum of axis_dim; channels from R on are not
+ * rotated.  Angles come from 64-bit fractions of a turn, so they stay exact to
+ * 2^-24 of a turn over all int32 positions (negative ones too).  The arithmetic
+ * is float32, rounded once to the tensors' type. */
+typedef struct {
+  int32_t n_axes;       /* 0 (no rotation) to 3 */
+  int32_t axis_dim[3];  /* even, >= 2 for axes < n_axes; their sum R <= head_dim */
+  int32_t halves;       /* 0: pairs of neighbours, 1: pairs R/2 apart (then R/2 is a
+                           multiple of 8 in bf16, of 4 in float32) */
+  float theta;          /* base of the rotation, in [1, 1e12] (ignored with n_axes = 0) */
+  float eps;            /* >= 0, finite */
+  const void* w_q;      /* device [head_dim] norm weights in the tensors' type, */
+  const void* w_k;      /* both null: no norm; one null is INVALID_ARGUMENT */
+} arl2_qk_prep;
+
+/* q_out, k_out = prep(q, k) for `tokens` tokens.
+ *   dtype    : ARL2_BF16 (head_dim a multiple of 8, <= 128) or ARL2_F32
+ *              (head_dim a multiple of 4, <= 128).
+ *   q, k     : device [tokens, heads, head_dim] and [tokens, kv_heads, head_dim];
+ *              token rows are ld elements apart (views into the rows of a
+ *              fused projection; 0: each contiguous), ld a multiple of 16 bytes.
+ *   pos      : device int32 [tokens, n_axes] (null when n_axes = 0).
+ *   q_out, k_out : the same shapes, token rows ld_out apart (0: contiguous).
+ *              An output may be its own input (equal pointer and pitch: in
+ *              place) and may otherwise share no byte with any input or the
+ *              other output -- except that two outputs, or an output and the
+ *              other input, may interleave in the rows of one pitch, as Q and K
+ *              of a fused row do.
+ * tokens = 0 does nothing.  Errors: INVALID_ARGUMENT, UNSUPPORTED (head_dim, or
+ * R/2 with halves), CUDA. */
+arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t heads, int32_t kv_heads,
+                              int32_t head_dim, int64_t tokens, const void* q, const void* k, int64_t ld,
+                              const int32_t* pos, void* q_out, void* k_out, int64_t ld_out, void* stream);
+
+/* ---- Softmax layers on a paged KV cache -----------------------------------
+ * The cache of many streams in one pool of pages, next to the contiguous
+ * arl2_kv layers: streams of different lengths, chunks of one to many new
+ * tokens, shared key heads (grouped queries), and eviction.
+ *
+ * The pools are the caller's device memory in the handle's dtype, both
+ * [n_pages, kv_heads, page_size, head_dim], 16-byte aligned; they must outlive
+ * the handle.  Key j of a stream is row j % page_size of page pages[j / page_size].
+ * The handle owns work space only (fixed at init), and as everywhere must not
+ * be used from two streams at once: two captured graphs of one handle share it,
+ * so their replays must be ordered.
+ *
+ * A batch of streams lives in device memory and is read by the kernels alone,
+ * so that a captured graph may be replayed with other lengths and pages:
+ *   q_start : int32 [n_seqs + 1], the streams' first rows among the new tokens;
+ *             non-decreasing; rows from q_start[n_seqs] on are left as they were;
+ *   kv_len  : int32 [n_seqs], keys cached per stream, the new tokens' included;
+ *   pages   : int32 [n_seqs, pages_ld], the streams' pages in order (entries
+ *             past the last page are not read).
+ * The host gives bounds that size the launches: tokens (rows of the new-token
+ * tensors), max_q and max_kv (at least any stream's new tokens and kv_len).
+ * What the kernels find out of range they do not access: a stream whose rows
+ * or lengths break a bound is left out (its outputs stay as they were), a page
+ * number outside [0, n_pages) reads as zeros and is not written; both record
+ * ARL2_ERR_PAGE for arl2_paged_last_error. */
+typedef struct {
+  int32_t heads;        /* H query heads */
+  int32_t kv_heads;     /* Hk: divides heads; heads / kv_heads <= 64 */
+  int32_t head_dim;     /* bf16: 128; float32: a multiple of 4, <= 128 */
+  int32_t page_size;    /* a multiple of 8, <= 4096 */
+  int32_t n_pages;      /* >= 1; n_pages * kv_heads * page_size < 2^31 */
+  int32_t dtype;        /* arl2_dtype */
+  float softmax_scale;  /* 0 => 1/sqrt(head_dim) */
+} arl2_paged_config;
+
+typedef struct {
+  int32_t n_seqs;  /* 0: every call returns at once */
+  int32_t tokens;
+  int32_t max_q;
+  int32_t max_kv;
+  int32_t pages_ld;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* pages;
+} arl2_paged_batch;
+
+typedef struct arl2_paged* arl2_paged_t;
+
+arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_pool, void* stream,
+                            arl2_paged_t* out);
+
+/* Store the new tokens' K and V as the last rows of their streams (keys
+ * kv_len - n .. kv_len - 1 of a stream with n new tokens), with prep's norm and
+ * rotation of K in the same pass, and Q's into q_out.
+ *   prep  : null stores K as it is; then q and q_out must be null.
+ *   q, k, v : [tokens, H or Hk, head_dim], token rows ld elements apart (0:
+ *           contiguous); q and q_out may both be null.  pos: int32 [tokens, n_axes].
+ *   q_out : [tokens, H, head_dim] contiguous; may be q itself when q is
+ *           contiguous, and otherwise shares no byte with an input.
+ * Tokens before key 0 (kv_len < n) are ARL2_ERR_PAGE and not stored. */
+arl2_status arl2_paged_append(arl2_paged_t h, const arl2_paged_batch* batch, const arl2_qk_prep* prep, const void* q,
+                              const void* k, const void* v, int64_t ld, const int32_t* pos, void* q_out,
+                              void* stream);
+
+/* O = softmax(Q K^T * scale) V of the new tokens over their streams' cached keys.
+ *   mask_block m: 0: every new token sees all kv_len keys (a frame's pass).
+ *     m > 0: new token t (from 0) of a stream with n new tokens sees the keys
+ *     before the chunk and the chunk's blocks of m tokens up to its own:
+ *     keys < clamp(kv_len - n + (floor(t / m) + 1) * m, 0, kv_len).  m = 1 is
+ *     causal, m = tokens per frame is causal by frames.
+ *   q   : [tokens, H, head_dim], token rows ld_q elements apart (0: contiguous).
+ *   o   : [tokens, H, head_dim] contiguous, shares no byte with q, lse or the pools.
+ *   lse : float32 [tokens, H], log sum exp of a row's scaled logits; may be null.
+ * A row that sees no key gets O = 0 and lse = -inf.  K and V of the
+ * cached keys (those below kv_len) must be finite; what lies past kv_len in the
+ * pool is not used, whatever it is.  A query pass that is not to be kept appends to scratch pages of its
+ * own table, as the calls take the pages anew each time. */
+arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, const void* q, int64_t ld_q,
+                              int32_t mask_block, void* o, float* lse, void* stream);
+
+/* The attention weight that every cached key received from the new tokens,
+ * summed over their rows and the query heads of the key head, on top of the
+ * decayed sum so far:
+ *   w_out[b][hk][j] = decay * w_in[b][hk][j] + sum exp(q k_j * scale - lse[row])
+ * over the rows that see key j.  lse is arl2_paged_attend's for the same
+ * batch, q and mask_block (rows with lse = -inf add nothing).  w_in, w_out:
+ * float32 [n_seqs, Hk, w_ld], w_ld >= max_kv; w_out may be w_in (equal pointer)
+ * and otherwise shares no byte with it.  Entries from kv_len on are set to 0
+ * in w_out (not read in w_in), so that tokens appended later start from 0. */
+arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, const void* q, int64_t ld_q,
+                               int32_t mask_block, const float* lse, float decay, const float* w_in, float* w_out,
+                               int64_t w_ld, void* stream);
+
+/* Cut every stream to at most `budget` keys, per key head: the first `sink`
+ * and the last `recent` keys, and of the others the budget - sink - recent
+ * with the largest weights w_in (equal weights: the lower index; NaN counts as
+ * the lowest), in their old order.  A stream of at most budget keys keeps all.
+ * The kept K and V rows are copied to the pages of dst_pages (int32 [n_seqs,
+ * dst_ld], ceil(min(kv_len, budget) / page_size) used per stream), which must
+ * be pages that no stream of `batch` uses and no two entries may share; a
+ * destination page that the stream itself reads is ARL2_ERR_PAGE and not
+ * written.  The old pages stay as they are: they may be shared with other
+ * streams, and belong to the caller again afterwards.
+ *   w_out      : float32 [n_seqs, Hk, w_ld]: the kept keys' weights, then 0;
+ *                shares no byte with w_in.
+ *   kept       : int32 [n_seqs, Hk, budget]: the kept keys' old indices, then -1.
+ *   kv_len_out : int32 [n_seqs]: min(kv_len, budget).
+ * No output shares a byte with an input, another output or the batch's arrays.
+ * q_start, tokens and max_q of the batch are not used.
+ * budget >= 1, sink and recent >= 0, sink + recent <= budget. */
+arl2_status arl2_paged_evict(arl2_paged_t h, const arl2_paged_batch* batch, const float* w_in, int64_t w_ld,
+                             int32_t budget, int32_t sink, int32_t recent, const int32_t* dst_pages, int32_t dst_ld,
+                             float* w_out, int32_t* kept, int32_t* kv_len_out, void* stream);
+
+/* Synchronise the handle's last stream and return (and clear) the first error
+ * recorded by its kernels (ARL2_ERR_PAGE, ARL2_ERR_TIMEOUT), ARL2_OK if none. */
+arl2_status arl2_paged_last_error(arl2_paged_t h);
+int64_t arl2_paged_device_bytes(arl2_paged_t h);
+/* As arl2_state_set_wait_limit. */
+arl2_status arl2_paged_set_wait_limit(arl2_paged_t h, uint64_t limit_ns);
+arl2_status arl2_paged_destroy(arl2_paged_t h);
 
 /* ---- Hybrid attention block (the layer around the hot path) ----------------
  * One hybrid layer with the projections a DiT attention block puts around it
