@@ -101,9 +101,15 @@ struct PrepParams {
 cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cudaStream_t st);
 // Attention: CTAs of the launch and rows of one of their pieces at most, which
 // size the handle's work space; then the launches (attention, combine).
-int paged_attn_grid(int dtype, int sms);
-int paged_piece_rows(int dtype);
-cudaError_t launch_paged_attn(PagedAttnParams p, int dtype, int grid, cudaStream_t st);
+// (float32: two blocks to an SM with head dims up to 64)
+inline int paged_attn_grid(int dtype, int sms) { return dtype == ARL2_BF16 ? sms : 2 * sms; }
+inline int paged_piece_rows(int dtype) { return dtype == ARL2_BF16 ? 256 : 64; }
+cudaError_t launch_paged_attn_f32(PagedAttnParams p, int grid, cudaStream_t st);
+// bf16 operands travel by TMA: maps over the pools (made once) and the queries
+bool paged_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int page_size);
+bool paged_query_map(CUtensorMap* m, const void* q, int64_t tokens, int heads, int group, int64_t ld);
+cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                                   cudaStream_t st);
 cudaError_t launch_paged_weights(const PagedWeightParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t st);
 
@@ -283,6 +289,7 @@ struct PagedWalk {
   int b, blk;
   bool fresh, have;
   PagedSeg<Plan> seg;
+  PagedWalk() = default;
   __device__ explicit PagedWalk(const PagedRange& range, int n_qblk)
       : r(range), b(range.f / n_qblk), blk(range.f % n_qblk), fresh(true), have(false) {}
   __device__ bool next(const PagedSeqs& s, int n_qblk, int group, int kv_heads, int mask_block) {

@@ -119,6 +119,7 @@ struct arl2_paged {
   uint32_t* err;
   int64_t bytes;
   cudaStream_t last_stream;
+  CUtensorMap tm_k, tm_v;  // over the pools (bf16)
 };
 
 namespace {
@@ -285,6 +286,14 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
   h->wait_ns = kDefaultWaitNs;
   h->last_stream = static_cast<cudaStream_t>(stream);
   if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || h->sms < 1) h->sms = 1;
+  if (cfg->dtype == ARL2_BF16) {
+    const int64_t rows = int64_t(cfg->n_pages) * cfg->kv_heads * cfg->page_size;
+    if (!tensor_map_encoder() || !paged_pool_map(&h->tm_k, k_pool, rows, cfg->page_size) ||
+        !paged_pool_map(&h->tm_v, v_pool, rows, cfg->page_size)) {
+      free_paged(h);
+      return ARL2_ERR_NO_DEVICE;
+    }
+  }
   h->grid = paged_attn_grid(cfg->dtype, h->sms);
   const size_t pieces = 2 * size_t(h->grid), rows = paged_piece_rows(cfg->dtype);
   const size_t po = pieces * rows * cfg->head_dim * sizeof(float), pm = pieces * rows * sizeof(float2);
@@ -415,7 +424,8 @@ arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, con
   p.rec = h->rec;
   p.err = h->err;
   p.wait_limit_ns = h->wait_ns;
-  PAGED_TRY(launch_paged_attn(p, c.dtype, h->grid, h->last_stream));
+  PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_attn_bf16(p, h->tm_k, h->tm_v, h->grid, h->last_stream)
+                                 : launch_paged_attn_f32(p, h->grid, h->last_stream));
   return ARL2_OK;
 }
 
