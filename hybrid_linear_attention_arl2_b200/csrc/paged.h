@@ -58,6 +58,8 @@ struct PagedWeightParams {
   int32_t heads, kv_heads, group, d;
   int32_t mask_block;
   float scale_log2;
+  float* part_w;        // bf16: [2 * grid][256] sums of key blocks that CTAs share
+  int4* rec;            // [2 * grid] (stream, key head, key block, starts | ends << 1) of those pieces
   uint32_t* err;
   uint64_t wait_limit_ns;
 };
@@ -110,7 +112,8 @@ bool paged_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int page_siz
 bool paged_query_map(CUtensorMap* m, const void* q, int64_t tokens, int heads, int group, int64_t ld);
 cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                                    cudaStream_t st);
-cudaError_t launch_paged_weights(const PagedWeightParams& p, int dtype, int sms, cudaStream_t st);
+cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st);
+cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensorMap& tk, int sms, cudaStream_t st);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t st);
 
 #ifdef __CUDACC__

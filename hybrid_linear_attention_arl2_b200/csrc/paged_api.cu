@@ -475,7 +475,10 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
   p.scale_log2 = h->scale * 1.4426950408889634f;
   p.err = h->err;
   p.wait_limit_ns = h->wait_ns;
-  PAGED_TRY(launch_paged_weights(p, c.dtype, h->sms, h->last_stream));
+  p.part_w = h->part_o;
+  p.rec = h->rec;
+  PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_weights_bf16(p, h->tm_k, h->sms, h->last_stream)
+                                 : launch_paged_weights_f32(p, h->last_stream));
   return ARL2_OK;
 }
 

@@ -1,6 +1,5 @@
 // Paged KV cache on CUDA cores (float32 tensors): attention of new tokens over
-// the pages, the weights the cached keys received, and the kernel that joins
-// the pieces of items cut by the CTAs' ranges (both types).
+// the pages, and the weights the cached keys received.
 //
 //   O = softmax(Q K^T scale) V over the visible keys,  lse = log sum exp,
 //   w_out[j] = decay w_in[j] + sum over rows of exp(s_j - lse)
@@ -31,8 +30,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
 
 // Rows of keys [k0, k0 + 64) of stream b and head hk into dst[64][ld] as
 // float; keys at or past `end` and keys of pages that are none read as zeros.
-template <typename T>
-__device__ __forceinline__ void load_keys(float* dst, int ld, const T* pool, const PagedSeqs& s, int b, int hk,
+__device__ __forceinline__ void load_keys(float* dst, int ld, const float* pool, const PagedSeqs& s, int b, int hk,
                                           int kv_heads, int d, int k0, int end, uint32_t* err) {
   const int v4 = d >> 2;
   for (int i = threadIdx.x; i < kKeys * v4; i += kThreads) {
@@ -71,9 +69,9 @@ __host__ __device__ inline size_t smem_floats(int d) {
 }
 
 // DC: 64-column chunks of the head dimension a thread accumulates (d <= 64 DC).
-template <typename T, int DC>
+template <int DC>
 __global__ void __launch_bounds__(kThreads)
-paged_attn_kernel(const PagedAttnParams p) {
+paged_attn_f32_kernel(const PagedAttnParams p) {
   extern __shared__ float sm[];
   __shared__ long long sh[64];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
@@ -86,7 +84,7 @@ paged_attn_kernel(const PagedAttnParams p) {
                                                        gridDim.x, p.err, sh);
   if (tid < 2) p.rec[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   PagedWalk<Plan> walk(range, p.n_qblk);
   while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
     const PagedSeg<Plan>& s = walk.seg;
@@ -116,8 +114,8 @@ paged_attn_kernel(const PagedAttnParams p) {
     for (int j = s.u0; j < s.u1; ++j) {
       const int k0 = j * kKeys;
       __syncthreads();
-      load_keys(sK, ld, static_cast<const T*>(p.k_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
-      load_keys(sV, ld, static_cast<const T*>(p.v_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
+      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
+      load_keys(sV, ld, static_cast<const float*>(p.v_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
       __syncthreads();
       float acc[4][4];
       scores(sQ, sK, ld, d, ty, tx, acc);
@@ -188,7 +186,7 @@ paged_attn_kernel(const PagedAttnParams p) {
         const float4 x = make_float4(o[a][4 * c] * inv, o[a][4 * c + 1] * inv, o[a][4 * c + 2] * inv,
                                      o[a][4 * c + 3] * inv);
         if (whole)
-          store4(static_cast<T*>(p.o) + orow * d + col, x);
+          store4(static_cast<float*>(p.o) + orow * d + col, x);
         else
           store4(p.part_o + (int64_t(piece) * kRows + r) * d + col, x);
       }
@@ -206,15 +204,14 @@ paged_attn_kernel(const PagedAttnParams p) {
 // ------------------------------------------------------------------ weights
 // One CTA per (stream, key head, 64 keys): every new token's rows go past in
 // tiles of 64, a thread sums its 4 rows' weights of its 4 keys.
-template <typename T>
 __global__ void __launch_bounds__(kThreads)
-paged_weights_kernel(const PagedWeightParams p, int n_kt) {
+paged_weights_f32_kernel(const PagedWeightParams p, int n_kt) {
   extern __shared__ float sm[];
   __shared__ float part[16][kKeys];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
   float* sQ = sm;
   float* sK = sQ + kRows * ld;
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   const int qt = kRows / p.group;
   const long long items = (long long)p.s.n_seqs * p.kv_heads * n_kt;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -226,7 +223,7 @@ paged_weights_kernel(const PagedWeightParams p, int n_kt) {
     const float* in = p.w_in + (int64_t(b) * p.kv_heads + hk) * p.w_ld;
     if (k0 < v.kv) {
       __syncthreads();
-      load_keys(sK, ld, static_cast<const T*>(p.k_pool), p.s, b, hk, p.kv_heads, d, k0, v.kv, p.err);
+      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, b, hk, p.kv_heads, d, k0, v.kv, p.err);
       float w[4] = {0.f, 0.f, 0.f, 0.f};
       for (int t0 = 0; t0 < v.n; t0 += qt) {
         const int rows = min(qt, v.n - t0) * p.group;
@@ -267,42 +264,37 @@ paged_weights_kernel(const PagedWeightParams p, int n_kt) {
   }
 }
 
-template <typename T, int DC>
+template <int DC>
 cudaError_t launch_attn(PagedAttnParams p, int grid, cudaStream_t st) {
   static unsigned done = 0;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_kernel<T, DC>),
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_f32_kernel<DC>),
                                    int(smem_floats(128) * sizeof(float)), &done);
   if (e != cudaSuccess) return e;
   const int qt = kRows / p.group;
   p.n_qblk = (p.s.max_q + qt - 1) / qt;
   if ((long long)p.n_qblk * p.s.n_seqs >= (1LL << 31)) return cudaErrorInvalidValue;
-  paged_attn_kernel<T, DC><<<grid, kThreads, smem_floats(p.d) * sizeof(float), st>>>(p);
+  paged_attn_f32_kernel<DC><<<grid, kThreads, smem_floats(p.d) * sizeof(float), st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_combine<T, 1, kRows, kKeys>(p, grid, st);
-}
-
-template <typename T>
-cudaError_t launch_weights(const PagedWeightParams& p, cudaStream_t st) {
-  const int bytes = int(size_t(kRows + kKeys) * (p.d + 4) * sizeof(float));
-  static unsigned done = 0;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_kernel<T>),
-                                   int(size_t(kRows + kKeys) * 132 * sizeof(float)), &done);
-  if (e != cudaSuccess) return e;
-  const long long n_kt = (p.w_ld + kKeys - 1) / kKeys;
-  const long long items = n_kt * p.s.n_seqs * p.kv_heads;
-  const unsigned grid = unsigned(items < (1 << 20) ? items : (1 << 20));
-  paged_weights_kernel<T><<<grid, kThreads, bytes, st>>>(p, int(n_kt));
-  return cudaGetLastError();
+  return launch_combine<float, 1, kRows, kKeys>(p, grid, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_f32(PagedAttnParams p, int grid, cudaStream_t st) {
-  return p.d <= 64 ? launch_attn<float, 1>(p, grid, st) : launch_attn<float, 2>(p, grid, st);
+  return p.d <= 64 ? launch_attn<1>(p, grid, st) : launch_attn<2>(p, grid, st);
 }
 
-cudaError_t launch_paged_weights(const PagedWeightParams& p, int dtype, int, cudaStream_t st) {
-  return dtype == ARL2_BF16 ? launch_weights<__nv_bfloat16>(p, st) : launch_weights<float>(p, st);
+cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st) {
+  const int bytes = int(size_t(kRows + kKeys) * (p.d + 4) * sizeof(float));
+  static unsigned done = 0;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_f32_kernel),
+                                   int(size_t(kRows + kKeys) * 132 * sizeof(float)), &done);
+  if (e != cudaSuccess) return e;
+  const long long n_kt = (p.w_ld + kKeys - 1) / kKeys;
+  const long long items = n_kt * p.s.n_seqs * p.kv_heads;
+  const unsigned grid = unsigned(items < (1 << 20) ? items : (1 << 20));
+  paged_weights_f32_kernel<<<grid, kThreads, bytes, st>>>(p, int(n_kt));
+  return cudaGetLastError();
 }
 
 }  // namespace arl2
