@@ -79,43 +79,11 @@ __device__ __forceinline__ Work work_of(const PagedSeg<Plan>& s, int group, int 
   return w;
 }
 
-// The segment's loads and products in order.  Step i is a product: of half
-// t, unit u, with K (S) or V (PV).  In a dual segment the two halves' steps use
-// the same slot.  valid() skips the steps of units that a half has not.
-struct Step {
-  int i, t, u;
-  bool is_v;
-  __device__ explicit Step() : i(-1) {}
-  __device__ bool next(const Work& w) {
-    const int most = max(w.n[0], w.n[1]);
-    while (true) {
-      ++i;
-      if (i < 2) {
-        t = i, u = 0, is_v = false;
-      } else {
-        const int m = i - 2;
-        u = m >> 2;
-        if (u >= most) return false;
-        t = (m >> 1) & 1;
-        is_v = !(m & 1);
-        if (!is_v) ++u;
-      }
-      if (u < w.n[t]) return true;
-    }
-  }
-};
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
-  const bool ok = mbar_wait(bar, parity, w);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // ------------------------------------------------------------------ loads
 __device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                           const CUtensorMap* tm_v, const PagedRange& range, uint64_t* bars, uint8_t* sQ,
                                           uint8_t* sR, const WaitCtl& w) {
   const int lane = threadIdx.x & 31;
-  const int box = box_keys(p.s.page_size), boxes = 128 / box;
   const int qt = 128 / p.group;
   uint32_t ring = 0, k = 0;
   PagedWalk<Plan> walk(range, p.n_qblk);
@@ -132,49 +100,37 @@ __device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtens
           tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s.hk * p.group,
                       s.blk.q0 + s.blk.t0 + t * qt);
     }
-    // K and V tiles, one lane a box (both its halves); rows one load ahead
-    Step st, ahead;
-    const int mine = lane < boxes ? lane * box : 0;
-    auto row_of = [&](const Step& x) {
-      return lane < boxes
-                 ? box_row(p.s, s.b, wk.tile(x.t, x.u) * 128 + mine, s.blk.v.kv, s.hk, p.kv_heads, p.err)
-                 : 0;
-    };
-    auto skip = [&](Step& x) {  // a dual segment loads once for both halves: with the first that uses it
-      bool more;
-      do more = x.next(wk);
-      while (more && wk.dual && x.t == 1 && x.u < wk.n[0]);
-      return more;
-    };
-    bool more = skip(ahead);
-    int row = more ? row_of(ahead) : 0;
-    while (more) {
-      st = ahead;
-      const int cur = row;
-      more = skip(ahead);
-      if (more) row = row_of(ahead);
+    // K and V tiles in the order in which the products take them: a dual
+    // segment's K(u), V(u); else K(0), K(1), V(0), K(2), V(1), ... of its tiles
+    const int n = wk.dual ? wk.n[1] : wk.n[0] + wk.n[1], lag = wk.dual ? 0 : 1, j0 = wk.tile(0, 0);
+    BoxRows rk(p.s, s.b, s.blk.v.kv, s.hk, p.kv_heads, j0, j0 + n, p.err), rv = rk;
+    auto load = [&](BoxRows& rows, int i, const CUtensorMap* tm) {
       const uint32_t slot = ring % kRing;
-      if (ring >= kRing && !warp_wait(&bars[B_RE + slot], ((ring / kRing) - 1) & 1, w)) return;
+      if (ring >= kRing && !warp_wait(&bars[B_RE + slot], ((ring / kRing) - 1) & 1, w)) return false;
       if (lane == 0) mbar_expect_tx(&bars[B_RF + slot], kTile);
       __syncwarp();
-      if (lane < boxes) {
-        uint8_t* dst = sR + slot * kTile + mine * 128;
-        const CUtensorMap* tm = st.is_v ? tm_v : tm_k;
-        tma_load_3d(dst, tm, &bars[B_RF + slot], 0, cur, 0);
-        tma_load_3d(dst + kHalfTile, tm, &bars[B_RF + slot], 64, cur, 0);
-      }
+      rows.load(j0 + i, sR + slot * kTile, tm, &bars[B_RF + slot]);
       __syncwarp();
       ++ring;
+      return true;
+    };
+    for (int i = 0; i < n + lag; ++i) {
+      if (i < n && !load(rk, i, tm_k)) return;
+      if (i >= lag && !load(rv, i - lag, tm_v)) return;
     }
     ++k;
   }
 }
 
 // ------------------------------------------------------------------ products
+// One warp (see elect_one).  Its order, with S_t(u + 1) right behind PV_t(u), is the loader's.
 __device__ __forceinline__ void mma_role(const PagedAttnParams& p, const PagedRange& range, uint64_t* bars,
                                          uint8_t* sQ, uint8_t* sR, uint32_t tmem, const WaitCtl& w) {
-  const int lane = threadIdx.x & 31;
   const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+  const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024), dk = smem_desc_sw128(smem_u32(sR), 16, 1024);
+  const uint64_t dv = smem_desc_sw128(smem_u32(sR), kHalfTile, 1024);
+  const uint32_t el = elect_one();
+  const int lane = threadIdx.x & 31;
   uint32_t ring = 0, k = 0, pf = 0;  // pf: a parity bit for each half
   PagedWalk<Plan> walk(range, p.n_qblk);
   while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
@@ -182,54 +138,72 @@ __device__ __forceinline__ void mma_role(const PagedAttnParams& p, const PagedRa
     const Work wk = work_of(s, p.group, p.mask_block);
     if (wk.n[0] == 0 && wk.n[1] == 0) continue;
     if (!warp_wait(&bars[B_QF], k & 1, w)) return;
-    const int most = max(wk.n[0], wk.n[1]);
-    int s_left = wk.n[0] + wk.n[1];
-    int loads = 0;
-    Step st;
-    while (st.next(wk)) {
-      // ring position: in a dual segment K(u), V(u) at 2 u, 2 u + 1
-      const uint32_t pos = ring + (wk.dual ? 2 * st.u + (st.is_v ? 1 : 0) : loads);
-      ++loads;
+    const bool dual = uniform(wk.dual);
+    const int left = uniform(s.blk.v.kv - wk.tile(0, 0) * 128);  // keys from the first tile on
+    // S of half t, with the K tile in ring position pos; `last`: the tile's last use
+    auto scores = [&](int t, uint32_t pos, bool last) {
       const uint32_t slot = pos % kRing;
-      const bool last_use = !wk.dual || st.t == 1;
-      if (!warp_wait(&bars[B_RF + slot], (pos / kRing) & 1, w)) return;
-      uint8_t* tile = sR + slot * kTile;
-      if (st.is_v) {
-        const int k0 = wk.tile(st.t, st.u) * 128, valid = min(128, s.blk.v.kv - k0);
-        // (the first that uses the tile clears its rows past the stream's keys)
-        if ((valid & 15) && (!wk.dual || st.t == 0 || st.u >= wk.n[0])) {
-          const int r0 = valid, n = ((valid + 15) & ~15) - valid;
-          for (int i = lane; i < n * 16; i += 32)
-            *reinterpret_cast<uint4*>(tile + (i & 8 ? kHalfTile : 0) + (r0 + (i >> 4)) * 128 + (i & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
+      if (!warp_wait(&bars[B_RF + slot], (pos / kRing) & 1, w)) return false;
+      mma_tile(tmem + t * 128, dq + (dual ? t * (kTile >> 4) : 0), dk + slot * (kTile >> 4), id_s, el);
+      mma_commit_el(&bars[B_SF + t], el);
+      if (last) mma_commit_el(&bars[B_RE + slot], el);
+      return true;
+    };
+    // O += P V; `clear`: the tile's first use; `fin`: the half's last product
+    auto values = [&](int t, int u, uint32_t pos, bool clear, bool last, bool fin) {
+      const uint32_t slot = pos % kRing;
+      if (!warp_wait(&bars[B_RF + slot], (pos / kRing) & 1, w)) return false;
+      const int valid = min(128, left - (dual ? u : 2 * u + t) * 128);
+      if (clear && (valid & 15)) {  // rows past the stream's keys
+        uint8_t* tile = sR + slot * kTile;
+        for (int i = valid * 8 + lane; i < ((valid + 15) & ~15) * 8; i += 32) {
+          *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(tile + kHalfTile + i * 16) = make_uint4(0, 0, 0, 0);
         }
-        if (!warp_wait(&bars[B_PF + st.t], (pf >> st.t) & 1, w)) return;
-        pf ^= 1u << st.t;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dv = smem_desc_sw128(smem_u32(tile), kHalfTile, 1024);
-          const uint32_t lo = uint32_t(dv), hi = uint32_t(dv >> 32);
-          const uint32_t o = tmem + 256 + st.t * 128, a = tmem + st.t * 128;
-          const int steps = (valid + 15) >> 4;
-          for (int kk = 0; kk < steps; ++kk) mma_ts(o, a + kk * 8, lo + kk * 128, hi, id_o, kk > 0 || st.u > 0);
-          if (last_use) mma_commit(&bars[B_RE + slot]);
-          if (st.u + 1 == wk.n[st.t]) mma_commit(&bars[B_OF + st.t]);
-        }
-      } else {
-        if (lane == 0) {
-          const uint64_t dq = smem_desc_sw128(smem_u32(sQ + (wk.dual ? st.t * kTile : 0)), 16, 1024);
-          mma_tile(tmem + st.t * 128, dq, smem_desc_sw128(smem_u32(tile), 16, 1024), id_s);
-          mma_commit(&bars[B_SF + st.t]);
-          if (last_use) mma_commit(&bars[B_RE + slot]);
-          if (s_left == 1) mma_commit(&bars[B_QE]);
-        }
-        --s_left;
+        fence_async_smem();
+        __syncwarp();
       }
-      __syncwarp();
+      if (!warp_wait(&bars[B_PF + t], (pf >> t) & 1, w)) return false;
+      pf ^= 1u << t;
+      tc_fence_after();
+      const uint64_t b = dv + slot * (kTile >> 4);
+      const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128;
+      if (valid == 128) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id_o, kk > 0 || u > 0, el);
+      } else {
+        for (int kk = 0; kk * 16 < valid; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id_o, kk > 0 || u > 0, el);
+      }
+      if (last) mma_commit_el(&bars[B_RE + slot], el);
+      if (fin) mma_commit_el(&bars[B_OF + t], el);
+      return true;
+    };
+    if (dual) {
+      const int n0 = uniform(wk.n[0]), n1 = uniform(wk.n[1]);  // n0 <= n1: the first tile's tokens are the earlier ones
+      if (n0 > 0 && !scores(0, ring, false)) return;
+      if (!scores(1, ring, true)) return;
+      for (int u = 0; u < n1; ++u) {
+        const uint32_t kp = ring + 2 * u + 2, vp = ring + 2 * u + 1;
+        if (u + 1 == n1) mma_commit_el(&bars[B_QE], el);  // every S of the segment has been issued
+        if (u < n0 && !values(0, u, vp, true, false, u + 1 == n0)) return;
+        if (u + 1 < n0 && !scores(0, kp, false)) return;
+        if (!values(1, u, vp, u >= n0, true, u + 1 == n1)) return;
+        if (u + 1 < n1 && !scores(1, kp, true)) return;
+      }
+      ring += 2 * n1;
+    } else {
+      const int n = uniform(wk.n[0] + wk.n[1]);  // tile i belongs to half i & 1
+      if (!scores(0, ring, true)) return;
+      if (n > 1 && !scores(1, ring + 1, true)) return;
+      for (int i = 0; i < n; ++i) {
+        if (i + 2 == n || n == 1) mma_commit_el(&bars[B_QE], el);
+        // ring: K(0) K(1) V(0) K(2) V(1) K(3) ... V(n - 2) V(n - 1)
+        const uint32_t vp = ring + (n == 1 ? 1 : i + 2 < n ? 2 * i + 2 : n + i);
+        if (!values(i & 1, i >> 1, vp, true, true, i + 2 >= n)) return;
+        if (i + 2 < n && !scores(i & 1, ring + 2 * i + 3, true)) return;
+      }
+      ring += 2 * n;
     }
-    ring += wk.dual ? 2 * most : loads;
     ++k;
   }
 }
@@ -485,8 +459,8 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   // Every product has completed once a commit behind all of them has arrived:
   // only then are shared and tensor memory released.
   __syncwarp();
-  if (warp == 1 && lane == 0) {
-    mma_commit(&bars[B_DRAIN]);
+  if (warp == 1) {
+    mma_commit_el(&bars[B_DRAIN], elect_one());
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&bars[B_DRAIN], 0) && global_timer_ns() - t0 < 10000000ull) {
     }

@@ -13,24 +13,58 @@ namespace arl2 {
 constexpr uint32_t kTile = 32768;  // 128 rows x 128 bf16: two boxes of 64 columns
 constexpr uint32_t kHalfTile = 16384;
 
-// D (+)= A B, A in tensor memory (bf16 pairs), B MN-major in shared memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
-                                       uint32_t acc) {
+// The issuing warp runs its loop as one, so that descriptors stay in uniform
+// registers, and one lane of it issues: `el` is 1 in that lane.  (Issued from a
+// branch of one lane, the moves of the operands took longer than the products:
+// 85 to 125 clocks each where 64 suffice.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t el;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
+  return el;
+}
+// A value that is the same in all lanes, told to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// D (+)= A B^T, both in shared memory, for the elected lane.
+__device__ __forceinline__ void mma_ss_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc));
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el));
+}
+// D (+)= A B, A in tensor memory (bf16 pairs), B MN-major in shared memory.
+__device__ __forceinline__ void mma_ts_el(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc,
+                                          uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(el));
+}
+__device__ __forceinline__ void mma_commit_el(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
 }
 
 // D = A B^T over K = 128, both K-major tiles of 128 rows.
-__device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const uint32_t off = (kk >> 2) * (kHalfTile >> 4) + (kk & 3) * 2;
-    mma_ss(d, a + off, b + off, idesc, kk > 0);
+    mma_ss_el(d, a + off, b + off, idesc, kk > 0, el);
   }
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  const bool ok = mbar_wait(bar, parity, w);
+  return __all_sync(0xffffffffu, ok);
 }
 
 // 32 lanes x 16 columns of 32-bit values.
@@ -60,15 +94,60 @@ __host__ __device__ __forceinline__ int box_keys(int page_size) {
   return a;
 }
 
-// The pool row of the box at keys [k, k + box) of a stream, for the lane that
-// loads it; the row past the pool's last (zeros) where the stream has no key
-// there or its table no page.
-__device__ __forceinline__ int box_row(const PagedSeqs& s, int b, int k, int kv, int hk, int kv_heads, uint32_t* err) {
-  const int none = s.n_pages * kv_heads * s.page_size;
-  if (k >= kv) return none;
-  const int pg = page_of(s, b, k, err);
-  return pg < 0 ? none : (pg * kv_heads + hk) * s.page_size + k % s.page_size;
-}
+// The pool rows of a run of a stream's key tiles, fetched ahead: a warp's lanes
+// hold the boxes of 32 / boxes tiles in a row, and the page numbers of the ones
+// after them are on their way while these are used.  A box without a key, or
+// whose table entry is no page, gets the row past the pool's last, which reads
+// as zeros.
+struct BoxRows {
+  const int32_t* table;
+  int box, boxes, per, kv, page_size, n_pages, hk, kv_heads;
+  int first, end;  // tiles held, [first, first + per); none from end on
+  int row, ahead;  // this lane's box; the page number of its box `per` tiles on
+  uint32_t* err;
+
+  __device__ int key_of(int tile0) const {
+    const int lane = threadIdx.x & 31;
+    return lane < per * boxes ? tile0 * 128 + lane * box : 0x7fffffff;
+  }
+  __device__ int fetch(int tile0) const {
+    const int k = key_of(tile0);
+    return tile0 < end && k < kv ? table[k / page_size] : -1;
+  }
+  __device__ void turn(int tile0, int pg) {
+    const int k = key_of(tile0);
+    row = n_pages * kv_heads * page_size;
+    if (tile0 < end && k < kv) {
+      if (unsigned(pg) < unsigned(n_pages))
+        row = (pg * kv_heads + hk) * page_size + k % page_size;
+      else
+        record_error(err, kDevPage);
+    }
+    first = tile0;
+  }
+  // tiles [tile0, tile1) of stream b
+  __device__ BoxRows(const PagedSeqs& s, int b, int kv_, int hk_, int kv_heads_, int tile0, int tile1, uint32_t* err_)
+      : table(s.pages + int64_t(b) * s.pages_ld), box(box_keys(s.page_size)), boxes(128 / box), per(32 / boxes), kv(kv_),
+        page_size(s.page_size), n_pages(s.n_pages), hk(hk_), kv_heads(kv_heads_), end(tile1), err(err_) {
+    const int pg = fetch(tile0);
+    ahead = fetch(tile0 + per);
+    turn(tile0, pg);
+  }
+  // Loads a tile (tiles are asked for in order) into dst: two boxes of 64
+  // columns for each run of keys, by the lanes that hold them.
+  __device__ void load(int tile, uint8_t* dst, const CUtensorMap* tm, uint64_t* bar) {
+    if (tile >= first + per) {
+      turn(first + per, ahead);
+      ahead = fetch(first + per);
+    }
+    const int i = int(threadIdx.x & 31) - (tile - first) * boxes;
+    if (i >= 0 && i < boxes) {
+      uint8_t* d = dst + i * box * 128;
+      tma_load_3d(d, tm, bar, 0, row, 0);
+      tma_load_3d(d + kHalfTile, tm, bar, 64, row, 0);
+    }
+  }
+};
 
 // 2^x for a pair on the FMA pipe: x = n + f, n = round(x) in the low mantissa
 // bits after adding 1.5 * 2^23, 2^f by the polynomial of degree 4 through the

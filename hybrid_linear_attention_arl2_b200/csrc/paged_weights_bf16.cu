@@ -17,7 +17,7 @@
 // bits every time.
 //
 // Warps: 0 loads, 1 issues the products, 2 puts the rows' lse next to their
-// tile, 4-7 and 8-11 take key tiles 0 and 1.  Tensor memory: S^T of tile t,
+// tile; four warpgroups sum, one for each key tile and half of the columns.  Tensor memory: S^T of tile t,
 // buffer i at columns (2 t + i) 128.
 
 #include "layer.h"
@@ -28,12 +28,9 @@ namespace arl2 {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kKeys = 256;  // of a block
 constexpr int kQRing = 3;
-// registers a thread: at launch, and after the split between the control warps and the sums
-constexpr int kLaunchRegs = 168, kCtlRegs = 88, kSumRegs = 208;
-static_assert(128 * kCtlRegs + 256 * kSumRegs <= kThreads * kLaunchRegs, "register split too large");
 
 enum {
   B_KF = 0,              // [2] a block's K loaded (bytes)
@@ -41,14 +38,16 @@ enum {
   B_QF = 4,              // [kQRing] a Q tile loaded (bytes)
   B_QE = B_QF + kQRing,  // [kQRing] read (commit)
   B_LF = B_QE + kQRing,  // [kQRing] its rows' lse in shared memory (warp 2)
-  B_LE = B_LF + kQRing,  // [kQRing] read (8 warps)
+  B_LE = B_LF + kQRing,  // [kQRing] read (16 warps)
   B_SF = B_LE + kQRing,  // [t][2] S^T in tensor memory (commit)
-  B_SC = B_SF + 4,       // [t][2] read (4 warps)
-  B_DRAIN = B_SC + 4,
+  B_SC = B_SF + 4,       // [t][2] read (8 warps)
+  B_JF = B_SC + 4,       // [t] half 1's sums in shared memory (4 warps)
+  B_JE = B_JF + 2,       // [t] read (4 warps)
+  B_DRAIN = B_JE + 2,
   B_COUNT
 };
-constexpr int kSmem = 1024 + 2 * 2 * kTile + kQRing * kTile + kQRing * 512 + 8 * B_COUNT + 16;
-static_assert(kSmem <= 232448, "shared memory");
+constexpr int kSmem = 232448, kLayout = 2 * 2 * kTile + kQRing * kTile + kQRing * 512 + 1024 + 8 * B_COUNT + 16;
+static_assert(kLayout <= kSmem, "shared memory");
 
 // A stream's units.  Row tile rt holds tokens [rt qt, ...); key block jt is
 // seen from the first token that sees its first key on, by all tiles after that.
@@ -165,18 +164,18 @@ __device__ __forceinline__ Walk find_range(const PagedWeightParams& p, int qt, l
     long long all;
     const long long beg = base + scan(c, sh, all);
     if (c > 0 && u0 >= beg && u0 < beg + c) {
-      sh[16] = b0 + tid;
-      sh[17] = u0 - beg;
+      sh[24] = b0 + tid;
+      sh[25] = u0 - beg;
     }
     __syncthreads();
     base += all;
     if (u0 < base) break;
   }
-  w.u.b = int(sh[16]);
+  w.u.b = int(sh[24]);
   const Stream s(p.s, w.u.b, qt, nullptr);
   const long long per = s.units(p.mask_block, qt);
-  w.u.hk = int(sh[17] / per);
-  const long long off = sh[17] % per;
+  w.u.hk = int(sh[25] / per);
+  const long long off = sh[25] % per;
   // the key block: a second search over the stream's blocks
   base = 0;
   for (int j0 = 0; j0 < s.n_kb; j0 += kThreads) {
@@ -185,22 +184,17 @@ __device__ __forceinline__ Walk find_range(const PagedWeightParams& p, int qt, l
     long long all;
     const long long beg = base + scan(c, sh, all);
     if (c > 0 && off >= beg && off < beg + c) {
-      sh[18] = jt;
-      sh[19] = r0 + (off - beg);
+      sh[26] = jt;
+      sh[27] = r0 + (off - beg);
     }
     __syncthreads();
     base += all;
     if (off < base) break;
   }
-  w.u.jt = int(sh[18]);
-  w.u.rt = int(sh[19]);
+  w.u.jt = int(sh[26]);
+  w.u.rt = int(sh[27]);
   __syncthreads();
   return w;
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
-  const bool ok = mbar_wait(bar, parity, w);
-  return __all_sync(0xffffffffu, ok);
 }
 
 // Which slot of the Q ring a unit reads: units of neighbouring blocks that
@@ -222,48 +216,43 @@ __device__ __forceinline__ void load_role(const PagedWeightParams& p, const CUte
                                           Walk walk, int qt, uint64_t* bars, uint8_t* sK, uint8_t* sQ,
                                           const WaitCtl& w) {
   const int lane = threadIdx.x & 31;
-  const int box = box_keys(p.s.page_size), boxes = 128 / box;
   QSlot q;
   uint32_t blocks = 0;
-  while (walk.next(p, qt)) {
-    const Unit& u = walk.u;
-    if (u.first) {
-      const uint32_t i = blocks & 1;
-      int row[2];
+  bool more = walk.next(p, qt);
+  while (more) {  // a (stream, key head) at a time: its key tiles lie in a row
+    const int b = walk.u.b, hk = walk.u.hk;
+    BoxRows rows(p.s, b, walk.s.v.kv, hk, p.kv_heads, 2 * walk.u.jt, 2 * walk.s.n_kb, p.err);
+    for (; more && walk.u.b == b && walk.u.hk == hk; more = walk.next(p, qt)) {
+      const Unit& u = walk.u;
+      if (u.first) {
+        const uint32_t i = blocks & 1;
+        if (blocks >= 2 && !warp_wait(&bars[B_KE + i], ((blocks >> 1) - 1) & 1, w)) return;
+        if (lane == 0) mbar_expect_tx(&bars[B_KF + i], 2 * kTile);
+        __syncwarp();
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        row[t] = lane < boxes ? box_row(p.s, u.b, u.jt * kKeys + t * 128 + lane * box, walk.s.v.kv, u.hk, p.kv_heads, p.err)
-                              : 0;
-      if (blocks >= 2 && !warp_wait(&bars[B_KE + i], ((blocks >> 1) - 1) & 1, w)) return;
-      if (lane == 0) mbar_expect_tx(&bars[B_KF + i], 2 * kTile);
-      __syncwarp();
-      if (lane < boxes) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint8_t* dst = sK + (2 * i + t) * kTile + lane * box * 128;
-          tma_load_3d(dst, tm_k, &bars[B_KF + i], 0, row[t], 0);
-          tma_load_3d(dst + kHalfTile, tm_k, &bars[B_KF + i], 64, row[t], 0);
+        for (int t = 0; t < 2; ++t) rows.load(2 * u.jt + t, sK + (2 * i + t) * kTile, tm_k, &bars[B_KF + i]);
+        __syncwarp();
+        ++blocks;
+      }
+      if (q.step(u)) {
+        if (q.count > kQRing && !warp_wait(&bars[B_QE + q.slot()], q.parity() ^ 1, w)) return;
+        if (lane == 0) {
+          mbar_expect_tx(&bars[B_QF + q.slot()], 2u * uint32_t(qt * p.group) * 128u);
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sQ + q.slot() * kTile + h * kHalfTile, tm_q, &bars[B_QF + q.slot()], h * 64, hk * p.group,
+                        walk.s.v.q0 + u.rt * qt);
         }
+        __syncwarp();
       }
-      __syncwarp();
-      ++blocks;
-    }
-    if (q.step(u)) {
-      if (q.count > kQRing && !warp_wait(&bars[B_QE + q.slot()], q.parity() ^ 1, w)) return;
-      if (lane == 0) {
-        mbar_expect_tx(&bars[B_QF + q.slot()], 2u * uint32_t(qt * p.group) * 128u);
-        for (int h = 0; h < 2; ++h)
-          tma_load_3d(sQ + q.slot() * kTile + h * kHalfTile, tm_q, &bars[B_QF + q.slot()], h * 64, u.hk * p.group,
-                      walk.s.v.q0 + u.rt * qt);
-      }
-      __syncwarp();
     }
   }
 }
 
+// One warp (see elect_one).
 __device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, uint8_t* sK,
                                          uint8_t* sQ, uint32_t tmem, const WaitCtl& w) {
-  const int lane = threadIdx.x & 31;
+  const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024), dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+  const uint32_t el = elect_one();
   QSlot q;
   uint32_t blocks = 0, g = 0, old = 0;
   while (walk.next(p, qt)) {
@@ -274,24 +263,20 @@ __device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, 
     }
     const uint32_t i = (blocks - 1) & 1;
     if (q.step(u)) {
-      if (q.count > 1 && lane == 0) mma_commit(&bars[B_QE + old]);
+      if (q.count > 1) mma_commit_el(&bars[B_QE + old], el);
       old = q.slot();
       if (!warp_wait(&bars[B_QF + old], q.parity(), w)) return;
     }
-    const int rows = walk.rows(p, qt);
+    const int rows = uniform(walk.rows(p, qt));
     const uint32_t id = idesc_bf16(128, (rows + 15) & ~15, 0, 0), buf = g & 1;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (g >= 2 && !warp_wait(&bars[B_SC + 2 * t + buf], ((g >> 1) - 1) & 1, w)) return;
       tc_fence_after();
-      if (lane == 0) {
-        mma_tile(tmem + (2 * t + buf) * 128, smem_desc_sw128(smem_u32(sK + (2 * i + t) * kTile), 16, 1024),
-                 smem_desc_sw128(smem_u32(sQ + old * kTile), 16, 1024), id);
-        mma_commit(&bars[B_SF + 2 * t + buf]);
-        if (t == 1 && u.last) mma_commit(&bars[B_KE + i]);
-      }
-      __syncwarp();
+      mma_tile(tmem + (2 * t + buf) * 128, dk + (2 * i + t) * (kTile >> 4), dq + old * (kTile >> 4), id, el);
+      mma_commit_el(&bars[B_SF + 2 * t + buf], el);
     }
+    if (u.last) mma_commit_el(&bars[B_KE + i], el);
     ++g;
   }
 }
@@ -350,13 +335,15 @@ __device__ __forceinline__ float2 sum_chunk(const uint32_t* r, const float4* nl,
   return acc;
 }
 
+// Warpgroup (t, half): key tile t, columns [64 half, 64 half + 64) of each unit.
+// Half 1 hands its sums of a block to half 0 through sJ.
 __device__ __forceinline__ void sum_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, const float* sL,
-                                         uint32_t tmem, int t, const WaitCtl& w) {
+                                         float* sJ, uint32_t tmem, int t, int half, const WaitCtl& w) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
-  const uint32_t tS = tmem + t * 256 + (uint32_t(quarter * 32) << 16);
+  const uint32_t tS = tmem + t * 256 + half * 64 + (uint32_t(quarter * 32) << 16);
   const float2 sc = make_float2(p.scale_log2, p.scale_log2);
   QSlot q;
-  uint32_t g = 0, old = 0;
+  uint32_t g = 0, old = 0, blocks = 0;
   float sum = 0.f;
   while (walk.next(p, qt)) {
     const Unit& u = walk.u;
@@ -375,39 +362,52 @@ __device__ __forceinline__ void sum_role(const PagedWeightParams& p, Walk walk, 
     const bool masked = __any_sync(0xffffffffu, lo > 0) || rows < 128;
     const uint32_t buf = g & 1;
     if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
+    ++g;
     tc_fence_after();
-    uint32_t r[128];
-    const int chunks = (rows + 31) >> 5;
+    const float4* nl = reinterpret_cast<const float4*>(sL + old * 128 + half * 64);
+    float2 acc = make_float2(0.f, 0.f);
     // (columns from the product's width on hold an older product, and are masked)
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < chunks) tmem_ld32(tS + buf * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
-    tmem_wait_ld();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[B_SC + 2 * t + buf]);
-    ++g;
-    const float4* nl = reinterpret_cast<const float4*>(sL + old * 128);
-    float2 acc = make_float2(0.f, 0.f);
-    if (!masked) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc = sum_chunk<false>(&r[32 * c], nl + 8 * c, sc, 0, 0, 0, acc);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) acc = sum_chunk<true>(&r[32 * c], nl + 8 * c, sc, 32 * c, lo, rows, acc);
+    for (int c = 0; c < 2; ++c) {
+      uint32_t r[32];
+      const bool some = half * 64 + 32 * c < rows;
+      if (some) {
+        tmem_ld32(tS + buf * 128 + c * 32, r);
+        tmem_wait_ld();
+      }
+      if (c == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_SC + 2 * t + buf]);
+      }
+      if (!masked)
+        acc = sum_chunk<false>(r, nl + 8 * c, sc, 0, 0, 0, acc);
+      else if (some)
+        acc = sum_chunk<true>(r, nl + 8 * c, sc, half * 64 + 32 * c, lo, rows, acc);
     }
     sum += acc.x + acc.y;
     if (u.last) {
-      const bool whole = u.starts && u.ends;
-      const int piece = 2 * blockIdx.x + (u.head ? 0 : 1);
-      if (whole) {
-        const int64_t at = (int64_t(u.b) * p.kv_heads + u.hk) * p.w_ld + key;
-        if (key < walk.s.v.kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], sum);
+      if (half == 1) {
+        if (blocks > 0 && !warp_wait(&bars[B_JE + t], (blocks - 1) & 1, w)) return;
+        sJ[t * 128 + row] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_JF + t]);
       } else {
-        p.part_w[piece * kKeys + t * 128 + row] = sum;
-        if (t == 0 && row == 0) p.rec[piece] = make_int4(u.b, u.hk, u.jt, (u.starts ? 1 : 0) | (u.ends ? 2 : 0));
+        if (!warp_wait(&bars[B_JF + t], blocks & 1, w)) return;
+        sum += sJ[t * 128 + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_JE + t]);
+        const bool whole = u.starts && u.ends;
+        const int piece = 2 * blockIdx.x + (u.head ? 0 : 1);
+        if (whole) {
+          const int64_t at = (int64_t(u.b) * p.kv_heads + u.hk) * p.w_ld + key;
+          if (key < walk.s.v.kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], sum);
+        } else {
+          p.part_w[piece * kKeys + t * 128 + row] = sum;
+          if (t == 0 && row == 0) p.rec[piece] = make_int4(u.b, u.hk, u.jt, (u.starts ? 1 : 0) | (u.ends ? 2 : 0));
+        }
       }
+      ++blocks;
       sum = 0.f;
     }
   }
@@ -419,16 +419,22 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
                           const PagedWeightParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (the window begins on 1024 bytes; a layout that does not fit is refused)
+  if (size_t(smem - smem_raw) + kLayout > size_t(kSmem)) {
+    if (threadIdx.x == 0) record_error(p.err, kDevBadShape);
+    return;
+  }
   uint8_t* sK = smem;                // [2 blocks][2 tiles]
   uint8_t* sQ = smem + 4 * kTile;    // [kQRing]
   float* sL = reinterpret_cast<float*>(sQ + kQRing * kTile);  // [kQRing][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sL + kQRing * 128);
+  float* sJ = sL + kQRing * 128;  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sJ + 256);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, qt = 128 / p.group;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(&bars[i], i >= B_LE && i < B_LE + kQRing ? 8 : i >= B_SC && i < B_SC + 4 ? 4 : 1);
+      mbar_init(&bars[i], i >= B_LE && i < B_LE + kQRing ? 16 : i >= B_SC && i < B_JF ? 8 : i >= B_JF && i < B_DRAIN ? 4 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -444,22 +450,20 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const WaitCtl w{abort_flag, p.err, p.wait_limit_ns};
-  if (warp < 4) {
-    regs_dec<kCtlRegs>();
-    if (warp == 0)
-      load_role(p, &tm_q, &tm_k, walk, qt, bars, sK, sQ, w);
-    else if (warp == 1)
-      mma_role(p, walk, qt, bars, sK, sQ, tmem, w);
-    else if (warp == 2)
-      lse_role(p, walk, qt, bars, sL, w);
-  } else {
-    regs_inc<kSumRegs>();
-    sum_role(p, walk, qt, bars, sL, tmem, (warp >> 2) - 1, w);
+  if (warp == 0) {
+    load_role(p, &tm_q, &tm_k, walk, qt, bars, sK, sQ, w);
+  } else if (warp == 1) {
+    mma_role(p, walk, qt, bars, sK, sQ, tmem, w);
+  } else if (warp == 2) {
+    lse_role(p, walk, qt, bars, sL, w);
+  } else if (warp >= 4) {
+    const int wg = (warp >> 2) - 1;
+    sum_role(p, walk, qt, bars, sL, sJ, tmem, wg & 1, wg >> 1, w);
   }
   // shared and tensor memory are released once a commit behind every product has arrived
   __syncwarp();
-  if (warp == 1 && lane == 0) {
-    mma_commit(&bars[B_DRAIN]);
+  if (warp == 1) {
+    mma_commit_el(&bars[B_DRAIN], elect_one());
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&bars[B_DRAIN], 0) && global_timer_ns() - t0 < 10000000ull) {
     }
@@ -529,13 +533,6 @@ cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensor
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_bf16_kernel), kSmem, &done);
   if (e != cudaSuccess) return e;
-  static int regs = -1;
-  if (regs < 0) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, paged_weights_bf16_kernel)) != cudaSuccess) return e;
-    regs = fa.numRegs;
-  }
-  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the register split needs this count
   int ctas = 0;
   if (p.s.tokens > 0 && p.s.max_q > 0 && p.s.max_kv > 0) {
     CUtensorMap tq;
