@@ -4,24 +4,27 @@
 //
 // One CTA an SM walks its range of units (PagedPlan).  Query rows of a (stream,
 // key head) are the pairs (token, head of the group), so the heads that share
-// keys share their tile: a tile is 128 rows.  Two tiles are in flight, and each
-// softmax warpgroup owns one: S_t = Q_t K^T (128 x 128, fp32 in tensor memory),
-// P_t over S_t in place (bf16 pairs), O_t += P_t V.  While warpgroup 0 is on its
-// exponentials the tensor core does warpgroup 1's products and the other way
-// round.  A block with one tile (single tokens, a chunk's tail) takes two key
-// tiles at once instead: both halves hold the same queries, half t the key
-// tiles 2 u + t, and their (m, l, O) are joined at the end, so that a single row
-// keeps as many bytes in flight as 256 rows do.
+// keys share their tile: a tile is 128 rows.  Two tiles are in flight, a softmax
+// warpgroup each.  A block with one tile (single tokens, a chunk's tail) takes
+// two key tiles at once instead: both halves hold the same queries, half t the
+// key tiles 2 u + t, and their (m, l, O) are joined at the end, so that a single
+// row keeps as many bytes in flight as 256 rows do.
+//
+// A half's work goes in steps of 64 keys with two S in tensor memory, so that
+// S(i + 1) is there when the softmax of step i ends: S(i) = Q K^T (128 x 64,
+// fp32), P(i) over it in place (bf16 pairs), O += P(i) V.  With 128 keys a step
+// and one S a half each half waited for its own products (softmax 2800 clocks,
+// products and signals 1500, one after the other); the halves hid too little of
+// each other.  Order of products, which the loader's ring of 32 KB tiles (128
+// keys) follows:  S_0(0) S_1(0) S_0(1) S_1(1), then for each step i
+//   PV_0(i) S_0(i + 2) PV_1(i) S_1(i + 2).
+// S(i + 2) overwrites P(i) behind PV(i) in the pipe.
 //
 // Warps: 0 loads (Q by one box a tile, K and V by boxes inside pages, one lane a
-// box, page numbers fetched a tile ahead), 1 issues the products, 4-7 and 8-11
-// softmax, O's rescaling (only when a row's maximum grows by more than 8 in
-// log2 units: P <= 256), and the output.  A softmax thread has one row.
-// The issuer's order, which the loader's ring of 32 KB tiles follows, is
-//   S_0(0) S_1(0), then for each unit u:  PV_0(u) S_0(u+1) PV_1(u) S_1(u+1);
-// S_t(u + 1) overwrites P_t(u) behind PV_t(u) in the pipe, and its completion
-// stands for PV_t(u)'s, after which O_t may be rescaled.
-// Tensor memory: S_0 / P_0 [0,128), S_1 / P_1 [128,256), O_0 [256,384), O_1 [384,512).
+// box, page numbers fetched ahead), 1 issues the products, 2 describes the
+// segments, 4-7 and 8-11 softmax, O's rescaling (only when a row's maximum grows
+// by more than 8 in log2 units: P <= 256) and the output; a thread has one row.
+// Tensor memory: S_t, P_t of step i at t 128 + (i & 1) 64; O_t at 256 + t 128.
 //
 // Rounding: P and O to bf16 (half a step, 2^-8, each); S, m, l and O's sums are
 // fp32.  Rows of V past the stream's keys are cleared in shared memory before a
@@ -37,73 +40,116 @@ namespace arl2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRing = 5;
-// registers a thread: at launch, and after the split between the control warps and the softmax
-constexpr int kLaunchRegs = 168, kCtlRegs = 72, kSoftmaxRegs = 216;
-static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split too large");
+constexpr int kRing = 5, kSegs = 4;
 using Plan = PagedPlan<2, 128, 128>;
 
 enum {
-  B_QF = 0,            // Q tiles loaded (bytes)
-  B_QE,                // Q read by the segment's last S (commit)
-  B_SF,                // [2] S_t in tensor memory (commit)
-  B_PF = B_SF + 2,     // [2] P_t written (the warpgroup's 4 warps)
-  B_OF = B_PF + 2,     // [2] O_t final (commit)
-  B_MG = B_OF + 2,     // half 1's statistics in shared memory (4 warps)
-  B_MD,                // half 1's O read by warpgroup 0 (4 warps)
-  B_RF,                // [kRing] ring slot loaded (bytes)
-  B_RE = B_RF + kRing, // [kRing] ring slot read (commit)
-  B_DRAIN = B_RE + kRing,
+  B_QF = 0,              // Q tiles loaded (bytes)
+  B_QE,                  // Q read by the segment's last S (commit)
+  B_SF,                  // [t][2] S_t of a step in tensor memory (commit)
+  B_PF = B_SF + 4,       // [t][2] P_t of a step written (the warpgroup's 4 warps)
+  B_PD = B_PF + 4,       // [t] a step's product with V done (commit)
+  B_OF = B_PD + 2,       // [t] O_t final (commit)
+  B_MG = B_OF + 2,       // half 1's statistics in shared memory (4 warps)
+  B_MD,                  // half 1's O and statistics read by half 0 (4 warps)
+  B_RF,                  // [kRing] ring slot loaded (bytes)
+  B_RE = B_RF + kRing,   // [kRing] ring slot read (commit)
+  B_GF = B_RE + kRing,   // [kSegs] segment described
+  B_GE = B_GF + kSegs,   // [kSegs] description read (loader, issuer, 8 softmax warps)
+  B_DRAIN = B_GE + kSegs,
   B_COUNT
 };
 
-// Key tiles of a segment for each half: the units both walk.
-struct Work {
-  bool dual;   // two tiles of rows on the same key tiles; else one tile on alternate ones
-  int n[2];    // units each half takes part in
-  int j0;      // first unit
-  __device__ int tile(int t, int u) const { return dual ? j0 + u : 2 * (j0 + u) + t; }
+// A segment as the roles need it, written by one warp into a ring.
+struct Seg {
+  int more;            // 0: the CTA's range is done
+  int b, hk;           // stream, key head
+  int row0;            // first token row of the block in q and o
+  int tok0;            // its token within the stream's new ones
+  int n_new, kv;       // the stream's new tokens and cached keys
+  int dual;            // two tiles of rows on the same key tiles; else one tile on alternate ones
+  int n[2];            // units each half takes part in
+  int j0;              // first key tile (dual: of both; else of half 0, half 1's is the next)
+  int rows[2];         // rows of each half's tile
+  int f, flags, slot;  // item; 1: holds its first unit, 2: its last; slot of its piece
 };
-__device__ __forceinline__ Work work_of(const PagedSeg<Plan>& s, int group, int mask_block) {
-  Work w;
-  w.dual = s.blk.tiles == 2;
-  w.j0 = s.u0;
+
+__device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, int group, int mask_block) {
   const int qt = 128 / group;
-#pragma unroll
+  g.more = 1;
+  g.b = s.b, g.hk = s.hk;
+  g.row0 = s.blk.q0 + s.blk.t0;
+  g.tok0 = s.blk.t0;
+  g.n_new = s.blk.v.n, g.kv = s.blk.v.kv;
+  g.dual = s.blk.tiles == 2;
+  g.j0 = g.dual ? s.u0 : 2 * s.u0;
   for (int t = 0; t < 2; ++t) {
-    const int last = w.dual ? min((t + 1) * qt, s.blk.n_tok) : s.blk.n_tok;  // the tile's tokens end
+    const int last = g.dual ? min((t + 1) * qt, s.blk.n_tok) : s.blk.n_tok;  // the tile's tokens end
     const int nk = (visible_keys(s.blk.v, mask_block, s.blk.t0 + last - 1) + 127) >> 7;
-    const int units = w.dual ? nk : (nk + 1 - t) >> 1;
-    w.n[t] = max(0, min(units, s.u1) - s.u0);
+    const int units = g.dual ? nk : (nk + 1 - t) >> 1;
+    g.n[t] = max(0, min(units, s.u1) - s.u0);
+    g.rows[t] = (g.dual ? last - t * qt : last) * group;
   }
-  return w;
+  g.f = s.f;
+  g.flags = (s.starts() ? 1 : 0) | (s.ends() ? 2 : 0);
+  g.slot = s.slot();
+}
+
+// The segments as a role meets them.
+struct SegReader {
+  const Seg* ring;
+  uint64_t* bars;
+  uint32_t k = 0;
+  __device__ const Seg* next(const WaitCtl& w) {  // a whole warp; null at the end
+    if (!warp_wait(&bars[B_GF + k % kSegs], (k / kSegs) & 1, w)) return nullptr;
+    const Seg* g = &ring[k % kSegs];
+    return g->more ? g : nullptr;
+  }
+  __device__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars[B_GE + k % kSegs]);
+    ++k;
+  }
+};
+
+__device__ __forceinline__ void seg_role(const PagedAttnParams& p, const PagedRange& range, uint64_t* bars, Seg* ring,
+                                         const WaitCtl& w) {
+  PagedWalk<Plan> walk(range, p.n_qblk);
+  bool more = true;
+  for (uint32_t k = 0; more; ++k) {
+    more = walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block);
+    if (k >= kSegs && !mbar_wait(&bars[B_GE + k % kSegs], (k / kSegs - 1) & 1, w)) return;
+    Seg& g = ring[k % kSegs];
+    if (more)
+      describe(g, walk.seg, p.group, p.mask_block);
+    else
+      g.more = 0;
+    mbar_arrive(&bars[B_GF + k % kSegs]);
+  }
 }
 
 // ------------------------------------------------------------------ loads
 __device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                                          const CUtensorMap* tm_v, const PagedRange& range, uint64_t* bars, uint8_t* sQ,
+                                          const CUtensorMap* tm_v, SegReader segs, uint64_t* bars, uint8_t* sQ,
                                           uint8_t* sR, const WaitCtl& w) {
   const int lane = threadIdx.x & 31;
   const int qt = 128 / p.group;
   uint32_t ring = 0, k = 0;
-  PagedWalk<Plan> walk(range, p.n_qblk);
-  while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
-    const PagedSeg<Plan>& s = walk.seg;
-    const Work wk = work_of(s, p.group, p.mask_block);
-    if (wk.n[0] == 0 && wk.n[1] == 0) continue;
+  for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
+    const bool dual = s->dual;
+    if (s->n[0] == 0 && s->n[1] == 0) continue;
     if (k > 0 && !warp_wait(&bars[B_QE], (k - 1) & 1, w)) return;
     if (lane == 0) {
-      const uint32_t bytes = uint32_t(qt * p.group) * 128u;
-      mbar_expect_tx(&bars[B_QF], 2u * uint32_t(s.blk.tiles) * bytes);
-      for (int t = 0; t < s.blk.tiles; ++t)
+      const int tiles = dual ? 2 : 1;
+      mbar_expect_tx(&bars[B_QF], 2u * uint32_t(tiles) * uint32_t(qt * p.group) * 128u);
+      for (int t = 0; t < tiles; ++t)
         for (int h = 0; h < 2; ++h)
-          tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s.hk * p.group,
-                      s.blk.q0 + s.blk.t0 + t * qt);
+          tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s->hk * p.group, s->row0 + t * qt);
     }
     // K and V tiles in the order in which the products take them: a dual
     // segment's K(u), V(u); else K(0), K(1), V(0), K(2), V(1), ... of its tiles
-    const int n = wk.dual ? wk.n[1] : wk.n[0] + wk.n[1], lag = wk.dual ? 0 : 1, j0 = wk.tile(0, 0);
-    BoxRows rk(p.s, s.b, s.blk.v.kv, s.hk, p.kv_heads, j0, j0 + n, p.err), rv = rk;
+    const int n = dual ? s->n[1] : s->n[0] + s->n[1], lag = dual ? 0 : 1, j0 = s->j0;
+    BoxRows rk(p.s, s->b, s->kv, s->hk, p.kv_heads, j0, j0 + n, p.err), rv = rk;
     auto load = [&](BoxRows& rows, int i, const CUtensorMap* tm) {
       const uint32_t slot = ring % kRing;
       if (ring >= kRing && !warp_wait(&bars[B_RE + slot], ((ring / kRing) - 1) & 1, w)) return false;
@@ -123,88 +169,161 @@ __device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtens
 }
 
 // ------------------------------------------------------------------ products
-// One warp (see elect_one).  Its order, with S_t(u + 1) right behind PV_t(u), is the loader's.
-__device__ __forceinline__ void mma_role(const PagedAttnParams& p, const PagedRange& range, uint64_t* bars,
-                                         uint8_t* sQ, uint8_t* sR, uint32_t tmem, const WaitCtl& w) {
-  const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
-  const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024), dk = smem_desc_sw128(smem_u32(sR), 16, 1024);
-  const uint64_t dv = smem_desc_sw128(smem_u32(sR), kHalfTile, 1024);
-  const uint32_t el = elect_one();
-  const int lane = threadIdx.x & 31;
-  uint32_t ring = 0, k = 0, pf = 0;  // pf: a parity bit for each half
-  PagedWalk<Plan> walk(range, p.n_qblk);
-  while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
-    const PagedSeg<Plan>& s = walk.seg;
-    const Work wk = work_of(s, p.group, p.mask_block);
-    if (wk.n[0] == 0 && wk.n[1] == 0) continue;
-    if (!warp_wait(&bars[B_QF], k & 1, w)) return;
-    const bool dual = uniform(wk.dual);
-    const int left = uniform(s.blk.v.kv - wk.tile(0, 0) * 128);  // keys from the first tile on
-    // S of half t, with the K tile in ring position pos; `last`: the tile's last use
-    auto scores = [&](int t, uint32_t pos, bool last) {
-      const uint32_t slot = pos % kRing;
-      if (!warp_wait(&bars[B_RF + slot], (pos / kRing) & 1, w)) return false;
-      mma_tile(tmem + t * 128, dq + (dual ? t * (kTile >> 4) : 0), dk + slot * (kTile >> 4), id_s, el);
-      mma_commit_el(&bars[B_SF + t], el);
-      if (last) mma_commit_el(&bars[B_RE + slot], el);
-      return true;
-    };
-    // O += P V; `clear`: the tile's first use; `fin`: the half's last product
-    auto values = [&](int t, int u, uint32_t pos, bool clear, bool last, bool fin) {
-      const uint32_t slot = pos % kRing;
-      if (!warp_wait(&bars[B_RF + slot], (pos / kRing) & 1, w)) return false;
-      const int valid = min(128, left - (dual ? u : 2 * u + t) * 128);
-      if (clear && (valid & 15)) {  // rows past the stream's keys
-        uint8_t* tile = sR + slot * kTile;
-        for (int i = valid * 8 + lane; i < ((valid + 15) & ~15) * 8; i += 32) {
-          *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(tile + kHalfTile + i * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
-        __syncwarp();
-      }
-      if (!warp_wait(&bars[B_PF + t], (pf >> t) & 1, w)) return false;
-      pf ^= 1u << t;
-      tc_fence_after();
-      const uint64_t b = dv + slot * (kTile >> 4);
-      const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128;
-      if (valid == 128) {
+// A place in the ring and the parity of its fill.
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  __device__ void move(uint32_t n) {  // n < kRing
+    slot += n;
+    if (slot >= kRing) slot -= kRing, phase ^= 1u;
+  }
+  __device__ RingPos at(uint32_t n) const {
+    RingPos r = *this;
+    r.move(n);
+    return r;
+  }
+};
+
+struct Issuer {
+  uint64_t* bars;
+  uint8_t* sR;
+  uint32_t tmem, dq, dk, dv, el, pf;  // descriptors of Q, and of ring slot 0 as K and as V; P's parities, a bit each
+  const WaitCtl& w;
+
+  __device__ __forceinline__ bool loaded(const RingPos& r) const { return warp_wait(&bars[B_RF + r.slot], r.phase, w); }
+  __device__ __forceinline__ void release(const RingPos& r) const { mma_commit_el(&bars[B_RE + r.slot], el); }
+  // S of half t, keys [64 h, 64 h + 64) of the tile
+  __device__ __forceinline__ void scores(int t, int h, const RingPos& r, uint32_t q) const {
+    mma_tile(tmem + t * 128 + h * 64, q, dk + r.slot * (kTile >> 4) + h * (8192 >> 4), idesc_bf16(128, 64, 0, 0), el);
+    mma_commit_el(&bars[B_SF + 2 * t + h], el);
+  }
+  // O += P V over `valid` keys of the same
+  __device__ __forceinline__ bool values(int t, int h, const RingPos& r, int valid, bool first) {
+    if (!warp_wait(&bars[B_PF + 2 * t + h], (pf >> (2 * t + h)) & 1, w)) return false;
+    pf ^= 1u << (2 * t + h);
+    tc_fence_after();
+    const uint32_t id = idesc_bf16(128, 128, 0, 1);
+    const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128 + h * 64, b = dv + r.slot * (kTile >> 4) + h * (8192 >> 4);
+    if (uniform(valid >= 64)) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id_o, kk > 0 || u > 0, el);
-      } else {
-        for (int kk = 0; kk * 16 < valid; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id_o, kk > 0 || u > 0, el);
-      }
-      if (last) mma_commit_el(&bars[B_RE + slot], el);
-      if (fin) mma_commit_el(&bars[B_OF + t], el);
-      return true;
-    };
-    if (dual) {
-      const int n0 = uniform(wk.n[0]), n1 = uniform(wk.n[1]);  // n0 <= n1: the first tile's tokens are the earlier ones
-      if (n0 > 0 && !scores(0, ring, false)) return;
-      if (!scores(1, ring, true)) return;
-      for (int u = 0; u < n1; ++u) {
-        const uint32_t kp = ring + 2 * u + 2, vp = ring + 2 * u + 1;
-        if (u + 1 == n1) mma_commit_el(&bars[B_QE], el);  // every S of the segment has been issued
-        if (u < n0 && !values(0, u, vp, true, false, u + 1 == n0)) return;
-        if (u + 1 < n0 && !scores(0, kp, false)) return;
-        if (!values(1, u, vp, u >= n0, true, u + 1 == n1)) return;
-        if (u + 1 < n1 && !scores(1, kp, true)) return;
-      }
-      ring += 2 * n1;
+      for (int kk = 0; kk < 4; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
     } else {
-      const int n = uniform(wk.n[0] + wk.n[1]);  // tile i belongs to half i & 1
-      if (!scores(0, ring, true)) return;
-      if (n > 1 && !scores(1, ring + 1, true)) return;
-      for (int i = 0; i < n; ++i) {
-        if (i + 2 == n || n == 1) mma_commit_el(&bars[B_QE], el);
-        // ring: K(0) K(1) V(0) K(2) V(1) K(3) ... V(n - 2) V(n - 1)
-        const uint32_t vp = ring + (n == 1 ? 1 : i + 2 < n ? 2 * i + 2 : n + i);
-        if (!values(i & 1, i >> 1, vp, true, true, i + 2 >= n)) return;
-        if (i + 2 < n && !scores(i & 1, ring + 2 * i + 3, true)) return;
-      }
-      ring += 2 * n;
+      for (int kk = 0; uniform(kk * 16 < valid); ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
     }
-    ++k;
+    mma_commit_el(&bars[B_PD + t], el);
+    return true;
+  }
+  // Clears a V tile's rows past the stream's keys (up to the product's 16).
+  __device__ __forceinline__ void clear(const RingPos& r, int valid) const {
+    if (uniform(valid < 128 && (valid & 15))) {
+      uint8_t* tile = sR + r.slot * kTile;
+      for (int x = valid * 8 + int(threadIdx.x & 31); x < ((valid + 15) & ~15) * 8; x += 32) {
+        *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(tile + kHalfTile + x * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      __syncwarp();
+    }
+  }
+};
+
+// One warp (see elect_one).
+__device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t* sQ, uint8_t* sR, uint32_t tmem,
+                                         const WaitCtl& w) {
+  Issuer x{bars, sR, tmem, desc_lo(sQ, 16), desc_lo(sR, 16), desc_lo(sR, kHalfTile), elect_one(), 0, w};
+  const uint32_t q1 = x.dq + (kTile >> 4);
+  RingPos ring;
+  uint32_t qf = 0;
+  for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
+    const int n0 = s->n[0], n1 = s->n[1];
+    int left = s->kv - s->j0 * 128;  // keys from the unit's first tile on
+    if (uniform(n0 == 0 && n1 == 0)) continue;
+    if (!warp_wait(&bars[B_QF], qf, w)) return;
+    qf ^= 1u;
+    if (uniform(s->dual)) {
+      // K(0) V(0) K(1) V(1) ...; n0 <= n1, as the first tile's tokens are the earlier ones
+      if (!x.loaded(ring)) return;
+      bool has0 = uniform(n0 > 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (has0) x.scores(0, h, ring, x.dq);
+        x.scores(1, h, ring, q1);
+      }
+      x.release(ring);
+      for (int u = 0;; ++u, left -= 128) {
+        const RingPos v = ring.at(1), k = ring.at(2);
+        const bool more0 = uniform(u + 1 < n0), more1 = uniform(u + 1 < n1);
+        if (!more1) mma_commit_el(&bars[B_QE], x.el);  // every S of the segment has been issued
+        if (!x.loaded(v)) return;
+        x.clear(v, left);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (has0 && !x.values(0, h, v, left - 64 * h, u == 0 && h == 0)) return;
+          if (more1 && h == 0 && !x.loaded(k)) return;
+          if (more0) x.scores(0, h, k, x.dq);
+          if (!x.values(1, h, v, left - 64 * h, u == 0 && h == 0)) return;
+          if (more1) x.scores(1, h, k, q1);
+        }
+        x.release(v);
+        if (has0 && !more0) mma_commit_el(&bars[B_OF], x.el);
+        ring.move(2);
+        if (!more1) break;
+        x.release(ring);
+        has0 = more0;
+      }
+      mma_commit_el(&bars[B_OF + 1], x.el);
+    } else {
+      // tiles y = 2 u + t: K(0) K(1) V(0) K(2) V(1) K(3) ... V(n - 2) V(n - 1)
+      const int n = n0 + n1;
+      const bool two = uniform(n1 > 0);
+      if (!x.loaded(ring)) return;
+      if (two && !x.loaded(ring.at(1))) return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x.scores(0, h, ring, x.dq);
+        if (two) x.scores(1, h, ring.at(1), x.dq);
+      }
+      x.release(ring);
+      if (two) x.release(ring.at(1));
+      ring.move(two ? 2 : 1);  // now at V(2 u)
+      for (int u = 0;; ++u, left -= 256) {
+        // units in pairs of tiles: V(2 u) [K(2 u + 2)] [V(2 u + 1)] [K(2 u + 3)]
+        const bool has1 = uniform(2 * u + 1 < n), more0 = uniform(2 * u + 2 < n), more1 = uniform(2 * u + 3 < n);
+        const RingPos v0 = ring, k0 = ring.at(1), v1 = ring.at(more0 ? 2 : 1), k1 = ring.at(3);
+        if (!more0) mma_commit_el(&bars[B_QE], x.el);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0) {
+            if (!x.loaded(v0)) return;
+            x.clear(v0, left);
+          }
+          if (!x.values(0, h, v0, left - 64 * h, u == 0 && h == 0)) return;
+          if (h == 1) x.release(v0);
+          if (more0) {
+            if (h == 0 && !x.loaded(k0)) return;
+            x.scores(0, h, k0, x.dq);
+            if (h == 1) x.release(k0);
+          }
+          if (has1) {
+            if (h == 0) {
+              if (!x.loaded(v1)) return;
+              x.clear(v1, left - 128);
+            }
+            if (!x.values(1, h, v1, left - 128 - 64 * h, u == 0 && h == 0)) return;
+            if (h == 1) x.release(v1);
+          }
+          if (more1) {
+            if (h == 0 && !x.loaded(k1)) return;
+            x.scores(1, h, k1, x.dq);
+            if (h == 1) x.release(k1);
+          }
+        }
+        if (has1 && !more1) mma_commit_el(&bars[B_OF + 1], x.el);
+        ring.move(1 + (more0 ? 1 : 0) + (has1 ? 1 : 0));
+        if (more1) ring.move(1);
+        if (!more0) break;
+      }
+      mma_commit_el(&bars[B_OF], x.el);
+    }
   }
 }
 
@@ -227,56 +346,36 @@ __device__ __forceinline__ float exp_chunk(const uint32_t* r, const float2 sc, c
   return sa.x + sa.y;
 }
 
-// A warp's walk, in shared memory: the rows' 128 logits leave no registers for it.
-struct SharedWalk {
-  PagedWalk<Plan> walk;
-  Work wk;
-  bool more;
-};
-
-constexpr int kSmem =
-    1024 + 2 * kTile + kRing * kTile + 8 * B_COUNT + 16 + 256 * 4 + 8 * int(sizeof(SharedWalk));
-static_assert(kSmem <= 232448, "shared memory");
-
-__device__ __forceinline__ void softmax_role(const PagedAttnParams& p, const PagedRange& range, uint64_t* bars,
-                                             float* stats, SharedWalk* sw, uint32_t tmem, int t, const WaitCtl& w) {
+// Warpgroup t: tile t's rows, one a thread, 64 keys a step.
+__device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader segs, uint64_t* bars, float* stats,
+                                             uint32_t tmem, int t, const WaitCtl& w) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
   const uint32_t lane_off = uint32_t(quarter * 32) << 16;
   const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * 128 + lane_off;
   const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-  const int qt = 128 / p.group;
-  uint32_t sf = 0, of = 0, merges = 0;
-  if (lane == 0) sw->walk = PagedWalk<Plan>(range, p.n_qblk);
-  while (true) {
-    __syncwarp();  // every lane is done with the previous segment
-    if (lane == 0) {
-      sw->more = sw->walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block);
-      if (sw->more) sw->wk = work_of(sw->walk.seg, p.group, p.mask_block);
-    }
-    __syncwarp();
-    if (!sw->more) return;
-    const PagedSeg<Plan>& s = sw->walk.seg;
-    const Work& wk = sw->wk;
-    const int tok0 = s.blk.t0 + (wk.dual ? t * qt : 0);
-    const int rows = (wk.dual ? min(qt, s.blk.n_tok - t * qt) : s.blk.n_tok) * p.group;
+  uint32_t g = 0, of = 0, merges = 0;  // g: steps so far
+  for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
+    const int rows = s->rows[t], n = 2 * s->n[t], skip = s->dual ? 0 : 128;
     const bool live = row < rows, warp_live = quarter * 32 < rows;
-    const int lim = live ? visible_keys(s.blk.v, p.mask_block, tok0 + row / p.group) : s.blk.v.kv;
+    int left = s->kv;  // visible keys from the step's first on
+    if (live)
+      left = visible_keys(SeqView{0, s->n_new, s->kv}, p.mask_block,
+                          s->tok0 + (s->dual ? t * (128 / p.group) : 0) + row / p.group);
+    left -= (s->j0 + (s->dual ? 0 : t)) * 128;
     float m = -INFINITY, l = 0.f;
-    const int n = wk.n[t], step = wk.dual ? 128 : 256;
-    int left = lim - wk.tile(t, 0) * 128;  // visible keys from the tile's first on
-    for (int u = 0; u < n; ++u, left -= step) {
-      if (!warp_wait(&bars[B_SF + t], sf & 1, w)) return;
-      ++sf;
+    for (int i = 0; i < n; ++i, ++g) {
+      const uint32_t buf = g & 1;  // (a segment has an even number of steps)
+      if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
       if (warp_live) {
         tc_fence_after();
-        uint32_t r[128];
+        uint32_t r[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+        for (int q = 0; q < 2; ++q) tmem_ld32(tS + buf * 64 + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * q]));
         tmem_wait_ld();
-        const bool masked = __any_sync(0xffffffffu, left < 128);
+        const bool masked = __any_sync(0xffffffffu, left < 64);
         if (masked) {
 #pragma unroll
-          for (int x = 0; x < 128; ++x)
+          for (int x = 0; x < 64; ++x)
             if (x >= left) r[x] = __float_as_uint(-INFINITY);
         }
         float m4[4];
@@ -284,43 +383,46 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, const Pag
         for (int q = 0; q < 4; ++q)
           m4[q] = fmax3(__uint_as_float(r[q]), __uint_as_float(r[4 + q]), __uint_as_float(r[8 + q]));
 #pragma unroll
-        for (int x = 12; x < 124; x += 8)
+        for (int x = 12; x < 60; x += 8)
 #pragma unroll
           for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(r[x + q]), __uint_as_float(r[x + 4 + q]));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], __uint_as_float(r[124 + q]));
+        for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], __uint_as_float(r[60 + q]));
         const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sc.x;
         const bool need = mx > m + 8.f;  // (also a row's first finite maximum)
         const float mg = need ? mx : m;
         const float ref = mg == -INFINITY ? 0.f : mg;  // nothing visible so far: every exponential is 0
-        const float f = fast_exp2(m - ref);
-        if (u > 0 && __any_sync(0xffffffffu, need)) {  // O *= 2^(old m - new m), 1 for rows that keep m
+        const float f = need ? fast_exp2(m - ref) : 1.f;
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          // O *= 2^(old m - new m), 1 for rows that keep m, once the step before is in O
+          if (!warp_wait(&bars[B_PD + t], (g - 1) & 1, w)) return;
+          tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
             uint32_t o[16];
             tmem_ld16(tO + q * 16, o);
             tmem_wait_ld();
-            const float g = need ? f : 1.f;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
             tmem_st16(tO + q * 16, o);
           }
         }
         const float2 nm = make_float2(-ref, -ref);
         float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t pc[16];
-          sum += masked ? exp_chunk<false>(&r[32 * c], sc, nm, pc) : exp_chunk<true>(&r[32 * c], sc, nm, pc);
-          tmem_st16(tS + c * 16, pc);
+          sum += masked ? exp_chunk<false>(&r[32 * q], sc, nm, pc) : exp_chunk<true>(&r[32 * q], sc, nm, pc);
+          tmem_st16(tS + buf * 64 + q * 16, pc);
         }
-        l = need ? fmaf(l, f, sum) : l + sum;
+        l = fmaf(l, f, sum);
         m = mg;
         tmem_wait_st();
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_PF + t]);
+      if (lane == 0) mbar_arrive(&bars[B_PF + 2 * t + buf]);
+      left -= 64 + (i & 1 ? skip : 0);
     }
     const bool have = n > 0;
     if (have) {
@@ -329,17 +431,19 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, const Pag
       tc_fence_after();
     }
     float a = 1.f, a1 = 0.f;  // O = a O_t + a1 O_1
-    const bool join = !wk.dual && wk.n[1] > 0;
-    if (join) {
-      if (t == 1) {  // warpgroup 0 writes the block's rows
+    const bool join = !s->dual && s->n[1] > 0;
+    if (!s->dual && t == 1) {  // half 0 writes the block's rows
+      if (join) {
         stats[row] = m;
         stats[128 + row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_MG]);
         if (!warp_wait(&bars[B_MD], merges & 1, w)) return;
         ++merges;
-        continue;
       }
+      continue;
+    }
+    if (join) {
       if (!warp_wait(&bars[B_MG], merges & 1, w)) return;
       ++merges;
       const float m1 = stats[row], l1 = stats[128 + row], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
@@ -347,51 +451,46 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, const Pag
       a1 = fast_exp2(m1 - ref);
       l = l * a + l1 * a1;
       m = M;
-    } else if (!wk.dual && t == 1) {
-      continue;
     }
-    const bool whole = s.whole();
-    const int piece = 2 * blockIdx.x + s.slot();
+    const bool whole = s->flags == 3;
+    const int piece = 2 * blockIdx.x + s->slot;
     if (whole) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       a *= inv, a1 *= inv;
     }
-    const int64_t orow = int64_t(s.blk.q0 + tok0 + row / p.group) * p.heads + s.hk * p.group + row % p.group;
+    const int64_t orow = int64_t(s->row0 + (s->dual ? t * (128 / p.group) : 0) + row / p.group) * p.heads +
+                         s->hk * p.group + row % p.group;
     const int64_t prow = int64_t(piece) * 256 + t * 128 + row;
-    if (!whole && t == 0 && row == 0) p.rec[piece] = make_int4(s.f, s.hk, s.starts(), s.ends());
+    if (!whole && t == 0 && row == 0) p.rec[piece] = make_int4(s->f, s->hk, s->flags & 1, s->flags >> 1);
     if (warp_live) {
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t o[32], o1[32];
-        if (have) tmem_ld32(tO + q * 32, o);
-        if (join) tmem_ld32(tO + 128 + q * 32, o1);
+      for (int q = 0; q < 8; ++q) {
+        uint32_t o[16], o1[16];
+        if (have) tmem_ld16(tO + q * 16, o);
+        if (join) tmem_ld16(tO + 128 + q * 16, o1);
         tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
+        for (int x = 0; x < 16; ++x) {
           float v = have ? __uint_as_float(o[x]) * a : 0.f;
           if (join) v = fmaf(__uint_as_float(o1[x]), a1, v);
           o[x] = __float_as_uint(v);
         }
         if (!live) continue;
         if (whole) {
-          char* dst = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32);
+          char* dst = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 16);
+          uint32_t v[8];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              v[x] = pack_bf16x2(__uint_as_float(o[c * 16 + 2 * x]), __uint_as_float(o[c * 16 + 2 * x + 1]));
-            if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
-              store_sector(dst + c * 32, v);
-            } else {
-              reinterpret_cast<uint4*>(dst + c * 32)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-              reinterpret_cast<uint4*>(dst + c * 32)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-            }
+          for (int x = 0; x < 8; ++x) v[x] = pack_bf16x2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
+          if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+            store_sector(dst, v);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
           }
         } else {
-          float* dst = p.part_o + prow * 128 + q * 32;
+          float* dst = p.part_o + prow * 128 + q * 16;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) store_sector(dst + c * 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[c * 8]));
+          for (int x = 0; x < 2; ++x) store_sector(dst + x * 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[x * 8]));
         }
       }
     }
@@ -409,25 +508,33 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, const Pag
   }
 }
 
+constexpr int kSmem = 232448;
+constexpr int kLayout = 2 * kTile + kRing * kTile + 256 * 4 + kSegs * int(sizeof(Seg)) + 8 * B_COUNT + 16;
+static_assert(kLayout <= kSmem, "shared memory");
+
 // ------------------------------------------------------------------ kernel
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (the window begins on 1024 bytes; a layout that does not fit is refused)
+  if (size_t(smem - smem_raw) + kLayout > size_t(kSmem)) {
+    if (threadIdx.x == 0) record_error(p.err, kDevBadShape);
+    return;
+  }
   uint8_t* sQ = smem;
   uint8_t* sR = smem + 2 * kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sR + kRing * kTile);
+  float* stats = reinterpret_cast<float*>(sR + kRing * kTile);  // half 1's m, l
+  Seg* segs = reinterpret_cast<Seg*>(stats + 256);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(segs + kSegs);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  long long* sh = reinterpret_cast<long long*>(tmem_holder + 4);
-  float* stats = reinterpret_cast<float*>(sh);  // [256], in the range search's words
-  SharedWalk* walks = reinterpret_cast<SharedWalk*>(stats + 256);  // of the 8 softmax warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const bool warps = i == B_PF || i == B_PF + 1 || i == B_MG || i == B_MD;
-      mbar_init(&bars[i], warps ? 4 : 1);
+      const int n = (i >= B_PF && i < B_PD) || i == B_MG || i == B_MD ? 4 : i >= B_GE && i < B_GE + kSegs ? 10 : 1;
+      mbar_init(&bars[i], n);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -440,21 +547,21 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   }
   if (threadIdx.x < 2) p.rec[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
   const PagedRange range = paged_range<Plan, kThreads>(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block, blockIdx.x,
-                                                       gridDim.x, p.err, sh);
+                                                       gridDim.x, p.err, reinterpret_cast<long long*>(stats));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const WaitCtl w{abort_flag, p.err, p.wait_limit_ns};
-  if (warp < 4) {
-    regs_dec<kCtlRegs>();
-    if (warp == 0)
-      load_role(p, &tm_q, &tm_k, &tm_v, range, bars, sQ, sR, w);
-    else if (warp == 1)
-      mma_role(p, range, bars, sQ, sR, tmem, w);
-  } else {
-    regs_inc<kSoftmaxRegs>();
-    softmax_role(p, range, bars, stats, walks + warp - 4, tmem, (warp >> 2) - 1, w);
+  const SegReader reader{segs, bars};
+  if (warp == 0) {
+    load_role(p, &tm_q, &tm_k, &tm_v, reader, bars, sQ, sR, w);
+  } else if (warp == 1) {
+    mma_role(reader, bars, sQ, sR, tmem, w);
+  } else if (warp == 2) {
+    if (lane == 0) seg_role(p, range, bars, segs, w);
+  } else if (warp >= 4) {
+    softmax_role(p, reader, bars, stats, tmem, (warp >> 2) - 1, w);
   }
   // Every product has completed once a commit behind all of them has arrived:
   // only then are shared and tensor memory released.
@@ -510,13 +617,6 @@ cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, con
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_bf16_kernel), kSmem, &done);
   if (e != cudaSuccess) return e;
-  static int regs = -1;
-  if (regs < 0) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, paged_attn_bf16_kernel)) != cudaSuccess) return e;
-    regs = fa.numRegs;
-  }
-  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the register split needs this count
   const int rows = 2 * (128 / p.group);
   p.n_qblk = (p.s.max_q + rows - 1) / rows;
   if ((long long)p.n_qblk * p.s.n_seqs >= (1LL << 31)) return cudaErrorInvalidValue;

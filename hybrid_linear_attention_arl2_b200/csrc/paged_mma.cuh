@@ -22,27 +22,39 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(el));
   return el;
 }
-// A value that is the same in all lanes, told to the compiler.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// A condition that is the same in all lanes, told to the compiler: what changes
+// under it stays in uniform registers.
+__device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
+
+// Shared-memory descriptors of 128-byte-swizzled tiles as (low word, shared high
+// word): the low word holds the address in units of 16 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(const void* smem, uint32_t lbo) {
+  return (smem_u32(smem) & 0x3FFFF) >> 4 | (lbo >> 4) << 16;
+}
 
 // D (+)= A B^T, both in shared memory, for the elected lane.
-__device__ __forceinline__ void mma_ss_el(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t el) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el));
-}
-// D (+)= A B, A in tensor memory (bf16 pairs), B MN-major in shared memory.
-__device__ __forceinline__ void mma_ts_el(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc,
+__device__ __forceinline__ void mma_ss_el(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc,
                                           uint32_t el) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(el));
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc), "r"(el));
+}
+// D (+)= A B, A in tensor memory (bf16 pairs), B MN-major in shared memory.
+__device__ __forceinline__ void mma_ts_el(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc,
+                                          uint32_t el) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc), "r"(el));
 }
 __device__ __forceinline__ void mma_commit_el(uint64_t* bar, uint32_t el) {
   asm volatile(
@@ -54,7 +66,7 @@ __device__ __forceinline__ void mma_commit_el(uint64_t* bar, uint32_t el) {
 }
 
 // D = A B^T over K = 128, both K-major tiles of 128 rows.
-__device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t el) {
+__device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t el) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const uint32_t off = (kk >> 2) * (kHalfTile >> 4) + (kk & 3) * 2;

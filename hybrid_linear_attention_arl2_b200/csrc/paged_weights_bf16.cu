@@ -251,7 +251,7 @@ __device__ __forceinline__ void load_role(const PagedWeightParams& p, const CUte
 // One warp (see elect_one).
 __device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, uint8_t* sK,
                                          uint8_t* sQ, uint32_t tmem, const WaitCtl& w) {
-  const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024), dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+  const uint32_t dk = desc_lo(sK, 16), dq = desc_lo(sQ, 16);
   const uint32_t el = elect_one();
   QSlot q;
   uint32_t blocks = 0, g = 0, old = 0;
@@ -267,7 +267,7 @@ __device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, 
       old = q.slot();
       if (!warp_wait(&bars[B_QF + old], q.parity(), w)) return;
     }
-    const int rows = uniform(walk.rows(p, qt));
+    const int rows = walk.rows(p, qt);
     const uint32_t id = idesc_bf16(128, (rows + 15) & ~15, 0, 0), buf = g & 1;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
