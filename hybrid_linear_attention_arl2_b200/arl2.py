@@ -533,28 +533,33 @@ class KVLayer:
             pass
 
 
-def _token_rows(heads, d, dtype, device, **tensors):
+def _bad_rows(name, t, h, d, dtype, index):
+    return ValueError(f"{name}: expected [tokens, {h}, {d}] of {dtype} on device {index} with contiguous token rows, got "
+                      f"{list(t.shape)} of {t.dtype} on {t.device} with strides {list(t.stride())}")
+
+
+def _token_rows(d, dtype, index, tensors):
     """The common pitch of [tokens, heads, head_dim] views in elements (0: each
-    contiguous), and their tokens; raises where the library cannot read them."""
+    contiguous), and their tokens, of (name, tensor, heads) triples; raises where
+    the library cannot read them."""
     ld = tokens = None
     dense = True
-    for name, t in tensors.items():
-        h = heads[name]
-        if t.dim() != 3 or t.shape[1] != h or t.shape[2] != d or t.dtype != dtype or t.device != device:
-            raise ValueError(f"{name}: expected [tokens, {h}, {d}] of {dtype} on {device}, "
-                             f"got {list(t.shape)} of {t.dtype} on {t.device}")
+    for name, t, h in tensors:
+        if t.dim() != 3 or t.dtype != dtype or t.get_device() != index:
+            raise _bad_rows(name, t, h, d, dtype, index)
+        n, th, td = t.shape
+        s0, s1, s2 = t.stride()
+        if th != h or td != d or s2 != 1 or (s1 != d and h > 1):
+            raise _bad_rows(name, t, h, d, dtype, index)
         if tokens is None:
-            tokens = t.shape[0]
-        elif t.shape[0] != tokens:
-            raise ValueError(f"{name}: {t.shape[0]} tokens, expected {tokens}")
-        s = t.stride()
-        if s[2] != 1 or (h > 1 and s[1] != d):
-            raise ValueError(f"{name}: a token's row must be contiguous")
-        if tokens > 1:
-            dense = dense and s[0] == h * d
+            tokens = n
+        elif n != tokens:
+            raise ValueError(f"{name}: {n} tokens, expected {tokens}")
+        if n > 1:
+            dense = dense and s0 == h * d
             if ld is None:
-                ld = s[0]
-            elif ld != s[0]:
+                ld = s0
+            elif ld != s0:
                 ld = -1
     if dense:
         return 0, tokens
@@ -563,17 +568,17 @@ def _token_rows(heads, d, dtype, device, **tensors):
     return ld, tokens
 
 
-def _plain(name, t, dtype, device, shape=None):
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+def _plain(name, t, dtype, index, shape=None):
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor{'' if shape is None else f' {list(shape)}'} on "
-                         f"{device}, got {list(t.shape)} of {t.dtype} on {t.device}")
+                         f"device {index}, got {list(t.shape)} of {t.dtype} on {t.device}")
     return t
 
 
-def _stream_of(device, stream):
+def _stream_of(index, stream):
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -594,33 +599,37 @@ class QKPrep:
         self.struct = arl2_qk_prep(len(axis_dims), (ctypes.c_int32 * 3)(*axis_dims), int(halves), theta, eps,
                                    _ptr(w_q), _ptr(w_k))
 
-    def _check(self, d, dtype, device, tokens, pos):
+    def _check(self, d, dtype, index, tokens, pos):
         import torch
-        for name, w in (("w_q", self.w_q), ("w_k", self.w_k)):
-            if w is not None:
-                _plain(name, w, dtype, device, (d,))
+        if self.w_q is not None:
+            _plain("w_q", self.w_q, dtype, index, (d,))
+            _plain("w_k", self.w_k, dtype, index, (d,))
         if self.n_axes:
             if pos is None:
                 raise ValueError("pos: the prep's axes need positions")
-            _plain("pos", pos, torch.int32, device, (tokens, self.n_axes))
+            _plain("pos", pos, torch.int32, index, (tokens, self.n_axes))
 
 
 def qk_norm_rope(prep: QKPrep, q, k, pos=None, q_out=None, k_out=None, stream=None):
     """Norm and rotate queries [tokens, heads, d] and keys [tokens, kv_heads, d]
     (views of one pitch, or contiguous) in one pass; returns (q_out, k_out)."""
     import torch
-    d, dev = q.shape[2], q.device
-    heads = {"q": q.shape[1], "k": k.shape[1]}
-    ld, tokens = _token_rows(heads, d, q.dtype, dev, q=q, k=k)
-    prep._check(d, q.dtype, dev, tokens, pos)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
-    ld_out, n = _token_rows(heads, d, q.dtype, dev, q=q_out, k=k_out)
+    tokens, h, d = q.shape
+    hk, dtype, index = k.shape[1], q.dtype, q.get_device()
+    ld, tokens = _token_rows(d, dtype, index, (("q", q, h), ("k", k, hk)))
+    prep._check(d, dtype, index, tokens, pos)
+    q_out = torch.empty((tokens, h, d), dtype=dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty((tokens, hk, d), dtype=dtype, device=q.device) if k_out is None else k_out
+    ld_out, n = _token_rows(d, dtype, index, (("q_out", q_out, h), ("k_out", k_out, hk)))
     if n != tokens:
         raise ValueError("outputs: as many tokens as the inputs")
-    with torch.cuda.device(dev):
-        arl2_qk_norm_rope(prep.struct, _abi_dtype(q.dtype), heads["q"], heads["k"], d, tokens, q, k, ld,
-                          pos if prep.n_axes else None, q_out, k_out, ld_out, _stream_of(dev, stream))
+    args = (prep.struct, _abi_dtype(dtype), h, hk, d, tokens, q, k, ld, pos if prep.n_axes else None, q_out, k_out,
+            ld_out, _stream_of(index, stream))
+    if torch._C._cuda_getDevice() == index:
+        arl2_qk_norm_rope(*args)
+    else:
+        with torch.cuda.device(index):
+            arl2_qk_norm_rope(*args)
     return q_out, k_out
 
 
@@ -643,11 +652,12 @@ class PagedBatch:
         n = kv_len.shape[0]
         if pages.dim() != 2 or pages.shape[0] != n:
             raise ValueError("pages: expected [streams, pages]")
-        _plain("kv_len", kv_len, torch.int32, kv_len.device, (n,))
-        _plain("q_start", q_start, torch.int32, kv_len.device, (n + 1,))
-        _plain("pages", pages, torch.int32, kv_len.device)
+        index = kv_len.get_device()
+        _plain("kv_len", kv_len, torch.int32, index, (n,))
+        _plain("q_start", q_start, torch.int32, index, (n + 1,))
+        _plain("pages", pages, torch.int32, index)
         self.q_start, self.kv_len, self.pages = q_start, kv_len, pages
-        self.tokens, self.device = tokens, kv_len.device
+        self.tokens, self.index = tokens, index
         self.struct = arl2_paged_batch(n, tokens, max_q, max_kv, pages.shape[1], _ptr(q_start), _ptr(kv_len),
                                        _ptr(pages))
 
@@ -659,103 +669,97 @@ class PagedKVLayer:
     def __init__(self, heads, kv_heads, head_dim, dtype, k_pool, v_pool, *, softmax_scale=0.0, stream=None):
         import torch
         self.handle = None
-        self.dtype, self.device = _torch_dtype(dtype), k_pool.device
+        self.dtype, self.device, self.index = _torch_dtype(dtype), k_pool.device, k_pool.get_device()
         if k_pool.dim() != 4 or k_pool.shape[1] != kv_heads or k_pool.shape[3] != head_dim:
             raise ValueError("k_pool: expected [n_pages, kv_heads, page_size, head_dim]")
-        _plain("k_pool", k_pool, self.dtype, self.device)
-        _plain("v_pool", v_pool, self.dtype, self.device, k_pool.shape)
+        _plain("k_pool", k_pool, self.dtype, self.index)
+        _plain("v_pool", v_pool, self.dtype, self.index, k_pool.shape)
         self.k_pool, self.v_pool = k_pool, v_pool
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.cfg = arl2_paged_config(heads, kv_heads, head_dim, k_pool.shape[2], k_pool.shape[0], dtype, softmax_scale)
         with torch.cuda.device(self.device):
-            self.handle = arl2_paged_init(self.cfg, k_pool, v_pool, _stream_of(self.device, stream))
+            self.handle = arl2_paged_init(self.cfg, k_pool, v_pool, _stream_of(self.index, stream))
 
-    def _batch(self, batch):
-        if batch.device != self.device:
-            raise ValueError(f"batch on {batch.device}, layer on {self.device}")
-        return batch.struct
-
-    def _rows(self, batch, **tensors):
-        heads = {"q": self.heads, "q_out": self.heads, "k": self.kv_heads, "v": self.kv_heads, "o": self.heads}
-        ld, tokens = _token_rows(heads, self.head_dim, self.dtype, self.device, **tensors)
-        if tokens != batch.tokens:
-            raise ValueError(f"{tokens} token rows, the batch has {batch.tokens}")
+    def _rows(self, batch, *tensors):
+        """The rows' pitch; checks them against the batch, and the batch's device."""
+        ld, tokens = _token_rows(self.head_dim, self.dtype, self.index, tensors)
+        if tokens != batch.tokens or batch.index != self.index:
+            raise ValueError(f"{tokens} token rows on device {self.index}; the batch has {batch.tokens} on {batch.index}")
         return ld
 
     def append(self, batch, k, v, *, q=None, prep=None, pos=None, q_out=None, stream=None):
         """Store the new tokens' K and V; with a prep, K normed and rotated, and
         q's turned rows are returned (q_out)."""
         import torch
-        st = self._batch(batch)
         if q is None:
             if q_out is not None:
                 raise ValueError("q_out without q")
-            ld = self._rows(batch, k=k, v=v)
+            ld = self._rows(batch, ("k", k, self.kv_heads), ("v", v, self.kv_heads))
         else:
             if prep is None:
                 raise ValueError("q without a prep")
-            ld = self._rows(batch, q=q, k=k, v=v)
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-            if self._rows(batch, q_out=q_out):
+            ld = self._rows(batch, ("q", q, self.heads), ("k", k, self.kv_heads), ("v", v, self.kv_heads))
+            if q_out is None:
+                q_out = torch.empty((batch.tokens, self.heads, self.head_dim), dtype=self.dtype, device=self.device)
+            elif self._rows(batch, ("q_out", q_out, self.heads)):
                 raise ValueError("q_out must be contiguous")
         if prep is not None:
-            prep._check(self.head_dim, self.dtype, self.device, batch.tokens, pos)
-        arl2_paged_append(self.handle, st, None if prep is None else prep.struct, q, k, v, ld,
-                          pos if prep is not None and prep.n_axes else None, q_out, _stream_of(self.device, stream))
+            prep._check(self.head_dim, self.dtype, self.index, batch.tokens, pos)
+        arl2_paged_append(self.handle, batch.struct, None if prep is None else prep.struct, q, k, v, ld,
+                          pos if prep is not None and prep.n_axes else None, q_out, _stream_of(self.index, stream))
         return q_out
 
     def attend(self, batch, q, *, mask_block=0, o=None, lse=None, stream=None):
         """(O, lse) of the new tokens over their streams' cached keys."""
         import torch
-        st = self._batch(batch)
-        ld = self._rows(batch, q=q)
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
-        if self._rows(batch, o=o):
+        ld = self._rows(batch, ("q", q, self.heads))
+        if o is None:
+            o = torch.empty((batch.tokens, self.heads, self.head_dim), dtype=self.dtype, device=self.device)
+        elif self._rows(batch, ("o", o, self.heads)):
             raise ValueError("o must be contiguous")
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+            lse = torch.empty((batch.tokens, self.heads), dtype=torch.float32, device=self.device)
         else:
-            _plain("lse", lse, torch.float32, self.device, q.shape[:2])
-        arl2_paged_attend(self.handle, st, q, ld, mask_block, o, lse, _stream_of(self.device, stream))
+            _plain("lse", lse, torch.float32, self.index, (batch.tokens, self.heads))
+        arl2_paged_attend(self.handle, batch.struct, q, ld, mask_block, o, lse, _stream_of(self.index, stream))
         return o, lse
 
     def _weights_shape(self, batch, w):
         import torch
-        if w.dim() != 3 or w.shape[0] != batch.struct.n_seqs or w.shape[1] != self.kv_heads:
-            raise ValueError(f"w: expected [{batch.struct.n_seqs}, {self.kv_heads}, keys], got {list(w.shape)}")
-        _plain("w", w, torch.float32, self.device)
+        n = batch.struct.n_seqs
+        if w.dim() != 3 or w.shape[0] != n or w.shape[1] != self.kv_heads or batch.index != self.index:
+            raise ValueError(f"w: expected [{n}, {self.kv_heads}, keys], got {list(w.shape)}")
+        _plain("w", w, torch.float32, self.index)
+        return n
 
     def weights(self, batch, q, lse, w, *, mask_block=0, decay=1.0, w_out=None, stream=None):
         """The cached keys' accumulated attention weights after the new tokens
         (w_out may be w)."""
         import torch
-        st = self._batch(batch)
-        ld = self._rows(batch, q=q)
+        ld = self._rows(batch, ("q", q, self.heads))
         self._weights_shape(batch, w)
-        _plain("lse", lse, torch.float32, self.device, q.shape[:2])
+        _plain("lse", lse, torch.float32, self.index, (batch.tokens, self.heads))
         if w_out is None:
-            w_out = torch.empty_like(w)
+            w_out = torch.empty(w.shape, dtype=torch.float32, device=self.device)
         else:
-            _plain("w_out", w_out, torch.float32, self.device, w.shape)
-        arl2_paged_weights(self.handle, st, q, ld, mask_block, lse, decay, w, w_out, w.shape[2],
-                           _stream_of(self.device, stream))
+            _plain("w_out", w_out, torch.float32, self.index, w.shape)
+        arl2_paged_weights(self.handle, batch.struct, q, ld, mask_block, lse, decay, w, w_out, w.shape[2],
+                           _stream_of(self.index, stream))
         return w_out
 
     def evict(self, batch, w, dst_pages, *, budget, sink=0, recent=0, stream=None):
         """Cut the streams to at most `budget` keys, moved to dst_pages; returns
         (kv_len, w, kept) of the streams in their new pages."""
         import torch
-        st = self._batch(batch)
-        self._weights_shape(batch, w)
-        n = batch.struct.n_seqs
+        n = self._weights_shape(batch, w)
         if dst_pages.dim() != 2 or dst_pages.shape[0] != n:
             raise ValueError("dst_pages: expected [streams, pages]")
-        _plain("dst_pages", dst_pages, torch.int32, self.device)
-        w_out = torch.empty_like(w)
+        _plain("dst_pages", dst_pages, torch.int32, self.index)
+        w_out = torch.empty(w.shape, dtype=torch.float32, device=self.device)
         kept = torch.empty((n, self.kv_heads, budget), dtype=torch.int32, device=self.device)
         kv_len = torch.empty((n,), dtype=torch.int32, device=self.device)
-        arl2_paged_evict(self.handle, st, w, w.shape[2], budget, sink, recent, dst_pages, dst_pages.shape[1], w_out,
-                         kept, kv_len, _stream_of(self.device, stream))
+        arl2_paged_evict(self.handle, batch.struct, w, w.shape[2], budget, sink, recent, dst_pages, dst_pages.shape[1],
+                         w_out, kept, kv_len, _stream_of(self.index, stream))
         return kv_len, w_out, kept
 
     def last_error(self) -> int:

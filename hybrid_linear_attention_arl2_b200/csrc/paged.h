@@ -15,6 +15,24 @@ namespace arl2 {
 constexpr uint32_t kDevPage = 9;  // ARL2_ERR_PAGE as kernels record it
 constexpr int kPagedMaxGroup = 64;
 
+// Division of numbers below 2^30 by a divisor known on the host: a product and a
+// shift.  With s = ceil(log2 d) - 2 and m = ceil(2^(32 + s) / d), m d - 2^(32 + s)
+// < d <= 2^(s + 2), so n m / 2^(32 + s) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t mul;
+  int32_t shift, by;
+  FastDiv() = default;
+  explicit FastDiv(int d) : mul(1), shift(0), by(d) {
+    if (d < 2) return;
+    int log = 0;
+    while ((1u << log) < unsigned(d)) ++log;
+    shift = 32 + log - 2;
+    mul = uint32_t(((uint64_t(1) << shift) + d - 1) / d);
+  }
+  __host__ __device__ int div(int n) const { return int((uint64_t(uint32_t(n)) * mul) >> shift); }
+  __host__ __device__ int mod(int n) const { return n - div(n) * by; }
+};
+
 // A batch as the kernels see it (arl2_paged_batch and the pool's extents).
 struct PagedSeqs {
   const int32_t* q_start;
@@ -22,7 +40,19 @@ struct PagedSeqs {
   const int32_t* pages;
   int32_t n_seqs, tokens, max_q, max_kv, pages_ld;
   int32_t page_size, n_pages;
+  FastDiv page;            // by page_size
+  int32_t box, boxes, per;  // keys of a TMA box, boxes of a 128-key tile, tiles that 32 boxes make (bf16)
 };
+
+// Keys per TMA box: the boxes of a 128-key tile lie inside pages.
+inline int box_keys(int page_size) {
+  int a = page_size, b = 128;
+  while (b) {
+    const int t = a % b;
+    a = b, b = t;
+  }
+  return a;
+}
 
 // Attention and weights: one launch's operands.
 struct PagedAttnParams {
@@ -35,12 +65,13 @@ struct PagedAttnParams {
   float* lse;           // [tokens, H] or null
   int32_t heads, kv_heads, group, d;
   int32_t mask_block;
+  FastDiv mask, per_group, per_blk;  // by mask_block, group, n_qblk
   float scale_log2;     // softmax scale * log2(e)
-  // work division (see PagedPlan): blocks of query rows per stream at most
-  int32_t n_qblk;
+  // work division (see PagedPlan): tokens of a tile, blocks of query rows per stream at most
+  int32_t qt, n_qblk;
   float* part_o;        // [2 * grid][rows][d] pieces of items that several CTAs share
   float2* part_ml;      // [2 * grid][rows] their running max (log2 units) and sum
-  int4* rec;            // [2 * grid] (f, kv head, starts, ends) of those pieces
+  uint32_t* joined;     // [grid][8] pieces of a CTA's cut item that are in (a count for each warp's rows); zero between launches
   uint32_t* err;
   uint64_t wait_limit_ns;
 };
@@ -57,6 +88,7 @@ struct PagedWeightParams {
   float decay;
   int32_t heads, kv_heads, group, d;
   int32_t mask_block;
+  FastDiv mask, per_group, per_tile;  // by mask_block, group, a tile's tokens
   float scale_log2;
   float* part_w;        // bf16: [2 * grid][256] sums of key blocks that CTAs share
   int4* rec;            // [2 * grid] (stream, key head, key block, starts | ends << 1) of those pieces
@@ -102,7 +134,7 @@ struct PrepParams {
 
 cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cudaStream_t st);
 // Attention: CTAs of the launch and rows of one of their pieces at most, which
-// size the handle's work space; then the launches (attention, combine).
+// size the handle's work space; then the launches.
 // (float32: two blocks to an SM with head dims up to 64)
 inline int paged_attn_grid(int dtype, int sms) { return dtype == ARL2_BF16 ? sms : 2 * sms; }
 inline int paged_piece_rows(int dtype) { return dtype == ARL2_BF16 ? 256 : 64; }
@@ -128,7 +160,7 @@ __device__ __forceinline__ SeqView load_seq(const PagedSeqs& s, int b, uint32_t*
   const int q0 = s.q_start[b], q1 = s.q_start[b + 1], kv = s.kv_len[b];
   SeqView v{q0, q1 - q0, kv};
   if (q0 < 0 || q1 < q0 || q1 > s.tokens || q1 - q0 > s.max_q || kv < 0 || kv > s.max_kv ||
-      (kv + s.page_size - 1) / s.page_size > s.pages_ld) {
+      kv > int64_t(s.pages_ld) * s.page_size) {
     if (err) atomicCAS(err, 0u, kDevPage);
     v = SeqView{0, -1, 0};
   }
@@ -138,7 +170,7 @@ __device__ __forceinline__ SeqView load_seq(const PagedSeqs& s, int b, uint32_t*
 // As load_seq for the calls that use a stream's cache alone.
 __device__ __forceinline__ int load_kv_len(const PagedSeqs& s, int b, uint32_t* err) {
   const int kv = s.kv_len[b];
-  if (kv < 0 || kv > s.max_kv || (kv + s.page_size - 1) / s.page_size > s.pages_ld) {
+  if (kv < 0 || kv > s.max_kv || kv > int64_t(s.pages_ld) * s.page_size) {
     if (err) atomicCAS(err, 0u, kDevPage);
     return -1;
   }
@@ -148,7 +180,7 @@ __device__ __forceinline__ int load_kv_len(const PagedSeqs& s, int b, uint32_t* 
 // The page that holds key j of stream b, or -1 (recorded) when the table's
 // entry is no page of the pool.  j < kv_len, so the entry exists.
 __device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int j, uint32_t* err) {
-  const int pg = s.pages[int64_t(b) * s.pages_ld + j / s.page_size];
+  const int pg = s.pages[int64_t(b) * s.pages_ld + s.page.div(j)];
   if (unsigned(pg) >= unsigned(s.n_pages)) {
     if (err) atomicCAS(err, 0u, kDevPage);
     return -1;
@@ -157,175 +189,177 @@ __device__ __forceinline__ int page_of(const PagedSeqs& s, int b, int j, uint32_
 }
 
 // Keys that new token t of a stream sees.
-__device__ __forceinline__ int visible_keys(const SeqView& v, int mask_block, int t) {
-  if (mask_block <= 0) return v.kv;
-  const long long lim = (long long)(v.kv - v.n) + (long long)(t / mask_block + 1) * mask_block;
+__device__ __forceinline__ int visible_keys(const SeqView& v, const FastDiv& mask, int t) {
+  if (mask.by <= 0) return v.kv;
+  const long long lim = (long long)(v.kv - v.n) + (long long)(mask.div(t) + 1) * mask.by;
   return lim < 0 ? 0 : lim > v.kv ? v.kv : int(lim);
 }
 
 // Division of an attention launch.  Query rows of one (stream, key head) are
-// the pairs (token, head of the group), token-major; a tile holds kTileRows /
-// group tokens, a block kTiles tiles.  Item (f, hk): f = b * n_qblk + block.
-// Its work is counted in units: with two tiles one unit is one tile of kKeys
-// keys against both; a block of one tile (single tokens) splits its keys
-// between the two halves of the CTA, so a unit is two key tiles.  Items lie in
-// a row, f first and key heads within it, and the CTAs take equal contiguous
-// ranges of the units: no CTA has more than one unit more than another,
-// however ragged the batch is.  An item cut by a range's end is finished by the
-// combine kernel from the CTAs' pieces: a CTA has at most two, one at its
-// range's begin (slot 0) and one at its end (slot 1).  An item has at least
-// one unit, so that rows which see no key get their zeros.
-template <int kTiles, int kTileRows, int kKeys>
+// the pairs (token, head of the group), token-major; a tile holds `qt` tokens, a
+// block kTiles tiles.  Item (f, hk): f = b * n_qblk + block.  Its work is counted
+// in units: with two tiles one unit is one tile of kKeys keys against both; a
+// block of one tile (single tokens) splits its keys between the two halves of
+// the CTA, so a unit is two key tiles.  Items lie in a row, f first and key heads
+// within it, and the CTAs take equal contiguous ranges of the units (no CTA has
+// more than one unit more than another, however ragged the batch is).  An item
+// cut by a range's end is finished from the CTAs' pieces by the one that comes
+// last: a CTA has at most two, one at its range's begin (slot 0) and one at its
+// end (slot 1).  An item has at least one unit, so that rows which see no key get
+// their zeros.  (The launch bounds the units below 2^31.)
+template <int kTiles, int kKeys>
 struct PagedPlan {
   struct Block {
-    int q0, t0, n_tok;  // stream's first row, the block's first token, its tokens (0: no item)
-    int tiles;          // 1 or 2
-    int units;          // per key head
-    SeqView v;
+    int row0, t0, n_tok;  // first token row, its token in the stream, tokens (0: no item)
+    int tiles;            // 1 or 2
+    int units;            // per key head
+    int n, kv;            // the stream's new tokens and cached keys
+    __device__ SeqView view() const { return SeqView{0, n, kv}; }
   };
-  __device__ static int tile_tokens(int group) { return kTileRows / group; }
-  __device__ static Block block(const PagedSeqs& s, int b, int blk, int group, int mask_block, uint32_t* err) {
+  __device__ static Block block(const PagedAttnParams& p, int f, uint32_t* err) {
     Block r;
-    r.v = load_seq(s, b, err);
-    const int qt = tile_tokens(group);
-    r.q0 = r.v.q0;
-    r.t0 = blk * qt * kTiles;
-    r.n_tok = r.v.n - r.t0;
+    const int b = p.per_blk.div(f);
+    const SeqView v = load_seq(p.s, b, err);
+    r.t0 = (f - b * p.n_qblk) * p.qt * kTiles;
+    r.row0 = v.q0 + r.t0;
+    r.n = v.n, r.kv = v.kv;
+    r.n_tok = min(v.n - r.t0, p.qt * kTiles);
+    r.tiles = kTiles == 2 && r.n_tok > p.qt ? 2 : 1;
+    r.units = 0;
     if (r.n_tok <= 0) {
       r.n_tok = 0;
-      r.tiles = 0;
-      r.units = 0;
       return r;
     }
-    if (r.n_tok > qt * kTiles) r.n_tok = qt * kTiles;
-    r.tiles = (r.n_tok + qt - 1) / qt;
-    int nk = (visible_keys(r.v, mask_block, r.t0 + r.n_tok - 1) + kKeys - 1) / kKeys;
-    if (kTiles == 2 && r.tiles == 1) nk = (nk + 1) >> 1;
-    r.units = nk < 1 ? 1 : nk;
+    const int nk = (visible_keys(v, p.mask, r.t0 + r.n_tok - 1) + kKeys - 1) / kKeys;
+    r.units = max(1, kTiles == 2 && r.tiles == 1 ? (nk + 1) >> 1 : nk);
     return r;
   }
 };
 
-// What a CTA walks: segments (f, hk, units [u0, u1) of the item).
-struct PagedRange {
-  int f, hk, u;          // where the range begins (u: unit within the item)
-  int left;              // units of the range
-};
-
-// Finds the CTA's range; called by all kThreads threads of the block.  Two
-// passes over the blocks of rows: their total, then the one that holds the
-// range's first unit.  `sh` is 64 shared 64-bit words.
-template <class Plan, int kThreads>
-__device__ __forceinline__ PagedRange paged_range(const PagedSeqs& s, int n_qblk, int group, int kv_heads,
-                                                  int mask_block, int cta, int grid, uint32_t* err,
-                                                  long long* sh) {
-  constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps + 8 <= 64, "shared words");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long F = (long long)s.n_seqs * n_qblk;
-  auto cost = [&](long long f) -> long long {
-    if (f >= F) return 0;
-    return (long long)Plan::block(s, int(f / n_qblk), int(f % n_qblk), group, mask_block, err).units * kv_heads;
-  };
-  long long first = cost(tid), sum = first;
-  for (long long f = tid + kThreads; f < F; f += kThreads) sum += cost(f);
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sh[warp] = sum;
-  __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < kWarps; ++w) total += sh[w];
-  const int ctas = total < grid ? int(total) : grid;
-  PagedRange r{0, 0, 0, 0};
-  if (cta >= ctas) return r;  // uniform over the block
-  const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-  r.left = int(u1 - u0);
-  __syncthreads();
-  long long base = 0;
-  for (long long f0 = 0; f0 < F; f0 += kThreads) {
-    const long long c = f0 == 0 ? first : cost(f0 + tid);
-    long long inc = c;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) sh[warp] = inc;
-    __syncthreads();
-    long long before = base, all = base;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sh[w];
-      all += sh[w];
-    }
-    const long long end = before + inc, beg = end - c;
-    if (c > 0 && u0 >= beg && u0 < end) {
-      sh[kWarps] = f0 + tid;
-      sh[kWarps + 1] = u0 - beg;
-      sh[kWarps + 2] = c / kv_heads;
-    }
-    __syncthreads();
-    if (u0 < all) break;
-    base = all;
-  }
-  r.f = int(sh[kWarps]);
-  const long long off = sh[kWarps + 1], units = sh[kWarps + 2];
-  r.hk = int(off / units);
-  r.u = int(off % units);
-  __syncthreads();
-  return r;
-}
-
-// One segment of the walk.
+// One segment of a CTA's walk: units [u0, u1) of item (f, hk).
 template <class Plan>
 struct PagedSeg {
   typename Plan::Block blk;
-  int b, f, hk, u0, u1;  // units [u0, u1) of item (f, hk)
-  bool first;            // the range's first segment
-  __device__ bool starts() const { return u0 == 0; }
-  __device__ bool ends() const { return u1 == blk.units; }
-  __device__ bool whole() const { return starts() && ends(); }
-  // the slot of a piece: the range's first segment has slot 0
-  __device__ int slot() const { return first ? 0 : 1; }
+  int f, hk, u0, u1;
+  // the item's pieces when it is cut: CTAs owner, owner + 1, ...; the owner's is in slot owner_slot, the others' in 0
+  int owner, pieces, owner_slot;
+  int slot;  // of this CTA's piece
+  __device__ bool whole() const { return pieces == 1; }
 };
 
 template <class Plan>
 struct PagedWalk {
-  PagedRange r;
-  int b, blk;
-  bool fresh, have;
+  int each, more;  // units of every range; the first `more` have one more
+  int pos, left;   // unit that comes next, units of the range that are left
+  bool have, fresh;
   PagedSeg<Plan> seg;
-  PagedWalk() = default;
-  __device__ explicit PagedWalk(const PagedRange& range, int n_qblk)
-      : r(range), b(range.f / n_qblk), blk(range.f % n_qblk), fresh(true), have(false) {}
-  __device__ bool next(const PagedSeqs& s, int n_qblk, int group, int kv_heads, int mask_block) {
-    if (r.left <= 0) return false;
-    if (!have) {
-      while (true) {
-        if (b >= s.n_seqs) return false;  // (cannot happen: the range lies inside the items)
-        seg.blk = Plan::block(s, b, blk, group, mask_block, nullptr);
-        if (seg.blk.units > 0) break;
-        if (++blk == n_qblk) blk = 0, ++b;
+
+  __device__ int begin(int cta) const { return each * cta + min(cta, more); }
+  __device__ int owner(int unit) const {  // the CTA whose range holds a unit
+    const int big = (each + 1) * more;
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+  }
+
+  // Finds the CTA's range; called by one warp.  Two passes over the blocks of
+  // rows: their total, then the one that holds the range's first unit.
+  __device__ __forceinline__ void find(const PagedAttnParams& p, int cta, int grid) {
+    const int lane = threadIdx.x & 31, F = p.s.n_seqs * p.n_qblk;
+    typename Plan::Block blk;
+    blk.units = 0;
+    int total = 0, mine = 0;
+    for (int f = lane; f < F; f += 32) {
+      blk = Plan::block(p, f, cta == 0 ? p.err : nullptr);
+      mine += blk.units;
+    }
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    total = mine * p.kv_heads;
+    const int ctas = min(total, grid);
+    left = 0;
+    have = fresh = true;
+    if (cta >= ctas) return;
+    each = total / ctas;
+    more = total - each * ctas;
+    pos = begin(cta);
+    left = begin(cta + 1) - pos;
+    int before = 0;
+    for (int f0 = 0; f0 < F; f0 += 32) {
+      if (F > 32) {
+        blk.units = 0;
+        if (f0 + lane < F) blk = Plan::block(p, f0 + lane, nullptr);
       }
+      const int c = f0 + lane < F ? blk.units * p.kv_heads : 0;
+      int inc = c;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int off = pos - (before + inc - c);
+      const unsigned hit = __ballot_sync(0xffffffffu, off >= 0 && off < c);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        const int at = __shfl_sync(0xffffffffu, off, src);
+        int* w = reinterpret_cast<int*>(&blk);
+        for (int i = 0; i < int(sizeof(blk) / 4); ++i) w[i] = __shfl_sync(0xffffffffu, w[i], src);
+        seg.blk = blk;
+        seg.f = f0 + src;
+        seg.hk = at / blk.units;
+        seg.u1 = at - seg.hk * blk.units;  // (the next segment begins at u1)
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    left = 0;  // (cannot happen: the range lies inside the items)
+  }
+
+  __device__ bool next(const PagedAttnParams& p) {
+    if (left <= 0) return false;
+    if (!have) {
+      const int F = p.s.n_seqs * p.n_qblk;
+      do {
+        if (++seg.f >= F) return false;  // (cannot happen)
+        seg.blk = Plan::block(p, seg.f, nullptr);
+      } while (seg.blk.units == 0);
+      seg.hk = 0;
       have = true;
     }
-    seg.b = b;
-    seg.f = b * n_qblk + blk;
-    seg.hk = r.hk;
-    seg.u0 = r.u;
-    const int rest = seg.blk.units - r.u;
-    const int take = rest < r.left ? rest : r.left;
-    seg.u1 = r.u + take;
-    seg.first = fresh;
-    fresh = false;
-    r.left -= take;
-    r.u = 0;
-    if (take == rest && ++r.hk == kv_heads) {
-      r.hk = 0;
-      have = false;
-      if (++blk == n_qblk) blk = 0, ++b;
+    seg.u0 = seg.u1;
+    const int take = min(seg.blk.units - seg.u0, left);
+    seg.u1 = seg.u0 + take;
+    seg.slot = fresh ? 0 : 1;
+    seg.owner = 0, seg.pieces = 1, seg.owner_slot = 0;
+    if (take < seg.blk.units) {
+      const int item = pos - seg.u0;
+      seg.owner = owner(item);
+      seg.pieces = owner(item + seg.blk.units - 1) - seg.owner + 1;
+      seg.owner_slot = begin(seg.owner) == item ? 0 : 1;
     }
+    fresh = false;
+    pos += take;
+    left -= take;
     return true;
   }
+  // After a segment's use: moves on to the next item where this one ended.
+  __device__ void done(const PagedAttnParams& p) {
+    if (seg.u1 < seg.blk.units) return;
+    seg.u1 = 0;
+    if (++seg.hk == p.kv_heads) have = false;
+  }
 };
-
 #endif  // __CUDACC__
+
+// Host side of the division: fills p's tile and block counts; false where the
+// units would not fit 31 bits.
+inline bool paged_plan(PagedAttnParams& p, int tile_rows, int tiles, int keys) {
+  p.qt = tile_rows / p.group;
+  const int64_t tokens = int64_t(p.qt) * tiles;
+  const int64_t n_qblk = (p.s.max_q + tokens - 1) / tokens;
+  if (n_qblk * p.s.n_seqs >= (int64_t(1) << 30)) return false;
+  if (double(n_qblk) * p.s.n_seqs * (p.s.max_kv / keys + 1) * p.kv_heads >= 2147483647.0) return false;
+  p.n_qblk = int32_t(n_qblk);
+  p.mask = FastDiv(p.mask_block);
+  p.per_group = FastDiv(p.group);
+  p.per_blk = FastDiv(p.n_qblk);
+  return true;
+}
 
 }  // namespace arl2

@@ -114,11 +114,14 @@ struct arl2_paged {
   uint64_t wait_ns;
   float* part_o;   // pieces of items that CTAs share, their statistics and records (PagedAttnParams)
   float2* part_ml;
-  int4* rec;
+  int4* rec;        // (weights)
+  uint32_t* joined;
   int grid;        // CTAs of the attention launch
   uint32_t* err;
   int64_t bytes;
   cudaStream_t last_stream;
+  FastDiv page;
+  int box;
   CUtensorMap tm_k, tm_v;  // over the pools (bf16)
 };
 
@@ -131,11 +134,13 @@ bool live(const arl2_paged* h) {
 }
 
 void free_paged(arl2_paged* h) {
-  for (void* p : {(void*)h->part_o, (void*)h->part_ml, (void*)h->rec, (void*)h->err})
+  for (void* p : {(void*)h->part_o, (void*)h->part_ml, (void*)h->rec, (void*)h->joined, (void*)h->err})
     if (p) cudaFree(p);
   h->magic = 0;
   delete h;
 }
+
+size_t joined_bytes(const arl2_paged* h) { return size_t(h->grid) * 8 * sizeof(uint32_t); }
 
 int group_of(const arl2_paged* h) { return h->cfg.heads / h->cfg.kv_heads; }
 
@@ -178,6 +183,10 @@ PagedSeqs seqs_of(const arl2_paged* h, const arl2_paged_batch* b) {
   s.pages_ld = b->pages_ld;
   s.page_size = h->cfg.page_size;
   s.n_pages = h->cfg.n_pages;
+  s.page = h->page;
+  s.box = h->box;
+  s.boxes = 128 / h->box;
+  s.per = 32 / s.boxes;
   return s;
 }
 
@@ -284,6 +293,8 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
   h->k_pool = k_pool;
   h->v_pool = v_pool;
   h->wait_ns = kDefaultWaitNs;
+  h->page = FastDiv(cfg->page_size);
+  h->box = box_keys(cfg->page_size);
   h->last_stream = static_cast<cudaStream_t>(stream);
   if (cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || h->sms < 1) h->sms = 1;
   if (cfg->dtype == ARL2_BF16) {
@@ -301,13 +312,15 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
   cudaError_t e = device_alloc(reinterpret_cast<void**>(&h->part_o), po);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->part_ml), pm);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->rec), pr);
+  if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->joined), joined_bytes(h));
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->joined, 0, joined_bytes(h), h->last_stream);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->err), 256);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 256, h->last_stream);
   if (e != cudaSuccess) {
     free_paged(h);
     return status_of_cuda(e);
   }
-  h->bytes = int64_t(po + pm + pr + 256);
+  h->bytes = int64_t(po + pm + pr + joined_bytes(h) + 256);
   h->magic = kPagedMagic;
   {
     std::lock_guard<std::mutex> g(g_paged_mu);
@@ -421,9 +434,11 @@ arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, con
   p.scale_log2 = h->scale * 1.4426950408889634f;
   p.part_o = h->part_o;
   p.part_ml = h->part_ml;
-  p.rec = h->rec;
+  p.joined = h->joined;
   p.err = h->err;
   p.wait_limit_ns = h->wait_ns;
+  if (!paged_plan(p, c.dtype == ARL2_BF16 ? 128 : 64, c.dtype == ARL2_BF16 ? 2 : 1, c.dtype == ARL2_BF16 ? 128 : 64))
+    return ARL2_ERR_UNSUPPORTED;
   PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_attn_bf16(p, h->tm_k, h->tm_v, h->grid, h->last_stream)
                                  : launch_paged_attn_f32(p, h->grid, h->last_stream));
   return ARL2_OK;
@@ -475,6 +490,9 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
   p.scale_log2 = h->scale * 1.4426950408889634f;
   p.err = h->err;
   p.wait_limit_ns = h->wait_ns;
+  p.mask = FastDiv(mask_block);
+  p.per_group = FastDiv(p.group);
+  p.per_tile = FastDiv(128 / p.group);
   p.part_w = h->part_o;
   p.rec = h->rec;
   PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_weights_bf16(p, h->tm_k, h->sms, h->last_stream)
@@ -543,7 +561,10 @@ arl2_status arl2_paged_last_error(arl2_paged_t h) {
   PAGED_TRY(cudaStreamSynchronize(h->last_stream));
   uint32_t w = 0;
   PAGED_TRY(cudaMemcpy(&w, h->err, sizeof(w), cudaMemcpyDeviceToHost));
-  if (w) PAGED_TRY(cudaMemset(h->err, 0, sizeof(w)));
+  if (w) {  // (a kernel that gave up may have left pieces counted)
+    PAGED_TRY(cudaMemset(h->err, 0, sizeof(w)));
+    PAGED_TRY(cudaMemset(h->joined, 0, joined_bytes(h)));
+  }
   return static_cast<arl2_status>(w);
 }
 

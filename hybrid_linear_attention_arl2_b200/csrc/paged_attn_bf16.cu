@@ -31,7 +31,7 @@
 // product sees them: what the pool holds there may be NaN.
 
 #include "layer.h"
-#include "paged_combine.cuh"
+#include "paged_join.cuh"
 #include "paged_mma.cuh"
 #include "params.h"
 
@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRing = 5, kSegs = 4;
-using Plan = PagedPlan<2, 128, 128>;
+using Plan = PagedPlan<2, 128>;
 
 enum {
   B_QF = 0,              // Q tiles loaded (bytes)
@@ -71,28 +71,34 @@ struct Seg {
   int n[2];            // units each half takes part in
   int j0;              // first key tile (dual: of both; else of half 0, half 1's is the next)
   int rows[2];         // rows of each half's tile
-  int f, flags, slot;  // item; 1: holds its first unit, 2: its last; slot of its piece
+  int slot;            // of this CTA's piece, and the pieces of the item (PagedSeg)
+  int owner, pieces, owner_slot;
 };
 
-__device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, int group, int mask_block) {
-  const int qt = 128 / group;
+__device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, const PagedAttnParams& p) {
+  const int qt = p.qt;
   g.more = 1;
-  g.b = s.b, g.hk = s.hk;
-  g.row0 = s.blk.q0 + s.blk.t0;
+  g.b = p.per_blk.div(s.f), g.hk = s.hk;
+  g.row0 = s.blk.row0;
   g.tok0 = s.blk.t0;
-  g.n_new = s.blk.v.n, g.kv = s.blk.v.kv;
+  g.n_new = s.blk.n, g.kv = s.blk.kv;
   g.dual = s.blk.tiles == 2;
   g.j0 = g.dual ? s.u0 : 2 * s.u0;
-  for (int t = 0; t < 2; ++t) {
-    const int last = g.dual ? min((t + 1) * qt, s.blk.n_tok) : s.blk.n_tok;  // the tile's tokens end
-    const int nk = (visible_keys(s.blk.v, mask_block, s.blk.t0 + last - 1) + 127) >> 7;
-    const int units = g.dual ? nk : (nk + 1 - t) >> 1;
-    g.n[t] = max(0, min(units, s.u1) - s.u0);
-    g.rows[t] = (g.dual ? last - t * qt : last) * group;
+  // the block's last token sees its key tiles; with two tiles the first may see fewer
+  const int all = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + s.blk.n_tok - 1) + 127) >> 7;
+  if (g.dual) {
+    const int nk = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + qt - 1) + 127) >> 7;
+    g.n[0] = max(0, min(nk, s.u1) - s.u0);
+    g.n[1] = max(0, min(all, s.u1) - s.u0);
+    g.rows[0] = qt * p.group;
+    g.rows[1] = (s.blk.n_tok - qt) * p.group;
+  } else {
+    g.n[0] = max(0, min((all + 1) >> 1, s.u1) - s.u0);
+    g.n[1] = max(0, min(all >> 1, s.u1) - s.u0);
+    g.rows[0] = g.rows[1] = s.blk.n_tok * p.group;
   }
-  g.f = s.f;
-  g.flags = (s.starts() ? 1 : 0) | (s.ends() ? 2 : 0);
-  g.slot = s.slot();
+  g.slot = s.slot;
+  g.owner = s.owner, g.pieces = s.pieces, g.owner_slot = s.owner_slot;
 }
 
 // The segments as a role meets them.
@@ -112,18 +118,21 @@ struct SegReader {
   }
 };
 
-__device__ __forceinline__ void seg_role(const PagedAttnParams& p, const PagedRange& range, uint64_t* bars, Seg* ring,
-                                         const WaitCtl& w) {
-  PagedWalk<Plan> walk(range, p.n_qblk);
+__device__ __forceinline__ void seg_role(const PagedAttnParams& p, uint64_t* bars, Seg* ring, const WaitCtl& w) {
+  PagedWalk<Plan> walk;
+  walk.find(p, blockIdx.x, gridDim.x);
+  if ((threadIdx.x & 31) != 0) return;
   bool more = true;
   for (uint32_t k = 0; more; ++k) {
-    more = walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block);
+    more = walk.next(p);
     if (k >= kSegs && !mbar_wait(&bars[B_GE + k % kSegs], (k / kSegs - 1) & 1, w)) return;
     Seg& g = ring[k % kSegs];
-    if (more)
-      describe(g, walk.seg, p.group, p.mask_block);
-    else
+    if (more) {
+      describe(g, walk.seg, p);
+      walk.done(p);
+    } else {
       g.more = 0;
+    }
     mbar_arrive(&bars[B_GF + k % kSegs]);
   }
 }
@@ -133,7 +142,7 @@ __device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtens
                                           const CUtensorMap* tm_v, SegReader segs, uint64_t* bars, uint8_t* sQ,
                                           uint8_t* sR, const WaitCtl& w) {
   const int lane = threadIdx.x & 31;
-  const int qt = 128 / p.group;
+  const int qt = p.qt;
   uint32_t ring = 0, k = 0;
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
     const bool dual = s->dual;
@@ -359,8 +368,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
     const bool live = row < rows, warp_live = quarter * 32 < rows;
     int left = s->kv;  // visible keys from the step's first on
     if (live)
-      left = visible_keys(SeqView{0, s->n_new, s->kv}, p.mask_block,
-                          s->tok0 + (s->dual ? t * (128 / p.group) : 0) + row / p.group);
+      left = visible_keys(SeqView{0, s->n_new, s->kv}, p.mask, s->tok0 + (s->dual ? t * p.qt : 0) + p.per_group.div(row));
     left -= (s->j0 + (s->dual ? 0 : t)) * 128;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i, ++g) {
@@ -452,53 +460,61 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
       l = l * a + l1 * a1;
       m = M;
     }
-    const bool whole = s->flags == 3;
-    const int piece = 2 * blockIdx.x + s->slot;
+    const bool whole = s->pieces == 1;
     if (whole) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       a *= inv, a1 *= inv;
     }
-    const int64_t orow = int64_t(s->row0 + (s->dual ? t * (128 / p.group) : 0) + row / p.group) * p.heads +
-                         s->hk * p.group + row % p.group;
-    const int64_t prow = int64_t(piece) * 256 + t * 128 + row;
-    if (!whole && t == 0 && row == 0) p.rec[piece] = make_int4(s->f, s->hk, s->flags & 1, s->flags >> 1);
+    const int tok_row = s->row0 + (s->dual ? t * p.qt : 0), head0 = s->hk * p.group;
+    auto out_row = [&](int r) { return int64_t(tok_row + p.per_group.div(r)) * p.heads + head0 + p.per_group.mod(r); };
+    const int64_t orow = out_row(row);
+    const int64_t prow = int64_t(2 * blockIdx.x + s->slot) * 256 + t * 128 + row;
     if (warp_live) {
+      // 32 columns at a time in a loop of its own: code that runs once costs its fetch
 #pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        uint32_t o[16], o1[16];
-        if (have) tmem_ld16(tO + q * 16, o);
-        if (join) tmem_ld16(tO + 128 + q * 16, o1);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32], o1[32];
+        tmem_ld32(tO + q * 32, o);
+        if (join) tmem_ld32(tO + 128 + q * 32, o1);
         tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < 32; ++x) {
           float v = have ? __uint_as_float(o[x]) * a : 0.f;
           if (join) v = fmaf(__uint_as_float(o1[x]), a1, v);
           o[x] = __float_as_uint(v);
         }
         if (!live) continue;
         if (whole) {
-          char* dst = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 16);
-          uint32_t v[8];
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = pack_bf16x2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
-          if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
-            store_sector(dst, v);
-          } else {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              v[x] = pack_bf16x2(__uint_as_float(o[c * 8 + 2 * x]), __uint_as_float(o[c * 8 + 2 * x + 1]));
+            dst[c] = make_uint4(v[0], v[1], v[2], v[3]);
           }
         } else {
-          float* dst = p.part_o + prow * 128 + q * 16;
+          float* dst = p.part_o + prow * 128 + q * 32;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) store_sector(dst + x * 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[x * 8]));
+          for (int c = 0; c < 4; ++c) store_sector(dst + c * 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[c * 8]));
         }
       }
-    }
-    if (live) {
-      if (!whole)
-        p.part_ml[prow] = make_float2(m, l);
-      else if (p.lse)
-        p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (live) {
+        if (!whole)
+          p.part_ml[prow] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+      if (!whole) {  // the warp whose piece of these rows comes last joins them
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = last_piece(p.joined + 8 * s->owner + 4 * t + quarter, s->pieces);
+        if (__shfl_sync(0xffffffffu, last, 0))
+          join_rows<__nv_bfloat16, 256>(p, s->owner, s->owner_slot, s->pieces, t * 128 + quarter * 32,
+                                        min(32, rows - quarter * 32), [&](int r) { return out_row(r - t * 128); });
+      }
     }
     if (join) {  // O_1 and its statistics are read
       tc_fence_before();
@@ -545,9 +561,6 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
   }
-  if (threadIdx.x < 2) p.rec[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
-  const PagedRange range = paged_range<Plan, kThreads>(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block, blockIdx.x,
-                                                       gridDim.x, p.err, reinterpret_cast<long long*>(stats));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -559,7 +572,7 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   } else if (warp == 1) {
     mma_role(reader, bars, sQ, sR, tmem, w);
   } else if (warp == 2) {
-    if (lane == 0) seg_role(p, range, bars, segs, w);
+    seg_role(p, bars, segs, w);
   } else if (warp >= 4) {
     softmax_role(p, reader, bars, stats, tmem, (warp >> 2) - 1, w);
   }
@@ -617,14 +630,10 @@ cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, con
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_bf16_kernel), kSmem, &done);
   if (e != cudaSuccess) return e;
-  const int rows = 2 * (128 / p.group);
-  p.n_qblk = (p.s.max_q + rows - 1) / rows;
-  if ((long long)p.n_qblk * p.s.n_seqs >= (1LL << 31)) return cudaErrorInvalidValue;
   CUtensorMap tq;
   if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
   paged_attn_bf16_kernel<<<grid, kThreads, kSmem, st>>>(tq, tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_combine<__nv_bfloat16, 2, 128, 128>(p, grid, st);
+  return cudaGetLastError();
 }
 
 }  // namespace arl2

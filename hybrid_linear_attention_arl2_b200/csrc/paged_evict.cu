@@ -4,10 +4,12 @@
 // Per stream and key head, of the kv keys between the first `sink` and the
 // last `recent` the m = budget - sink - recent with the largest weights stay.
 // Weights become whole numbers in the same order (NaN lowest, -0 equal to 0);
-// their m-th largest, T, is found by digits of 11, 11 and 10 bits from the top
-// (a histogram each, in shared memory), and keys above T stay, and as many of
-// those equal to T as are left, lowest index first.  The copy is bound by
-// bytes: each kept row in and out once.
+// their m-th largest, T, is found by digits of 11, 11 and 10 bits from the top,
+// and keys above T stay, and as many of those equal to T as are left, lowest
+// index first.  A cluster of CTAs takes a (stream, key head), a slice of its keys
+// each: a digit's histograms are summed by every CTA out of all the cluster's
+// shared memories, so that a digit costs one cluster barrier.  Then the copy,
+// bound by bytes: each kept row in and out once.
 
 #include "paged.h"
 #include "sm100.cuh"
@@ -17,7 +19,7 @@ namespace arl2 {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kCopyRows = 64, kCopyThreads = 256;
+constexpr int kCopyRows = 32, kCopyThreads = 256;
 constexpr int kBins = 2048;
 
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -47,39 +49,79 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* sh, int2& total) {
   return make_int2(base.x + inc.x - v.x, base.y + inc.y - v.y);
 }
 
-// One block per (stream, key head).
-__global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvictParams p) {
-  __shared__ int hist[kBins];
+constexpr int kHeld = 4;                      // keys a thread keeps in registers
+constexpr int kChunk = kThreads * kHeld;      // keys of a round
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ int remote_int(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+// One cluster per (stream, key head).
+__global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvictParams p, int cluster) {
+  __shared__ int hist[3][kBins];
   __shared__ int2 sh[kWarps];
   __shared__ int found[2];
-  const int b = blockIdx.x / p.kv_heads, hk = blockIdx.x % p.kv_heads, tid = threadIdx.x;
+  __shared__ int counts[2];
+  const int item = blockIdx.x / cluster, rank = blockIdx.x - item * cluster, tid = threadIdx.x;
+  const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
   const int kv = load_kv_len(p.s, b, p.err);
-  if (kv < 0) return;
+  if (kv < 0) return;  // (the whole cluster)
   const int64_t row = int64_t(b) * p.kv_heads + hk;
   const float* w = p.w_in + row * p.w_ld;
   float* wo = p.w_out + row * p.w_ld;
   int32_t* kept = p.kept + row * p.budget;
-  if (hk == 0 && tid == 0) p.kv_len_out[b] = kv < p.budget ? kv : p.budget;
+  const int step = cluster * kThreads, me = rank * kThreads + tid;
+  if (hk == 0 && me == 0) p.kv_len_out[b] = kv < p.budget ? kv : p.budget;
   if (kv <= p.budget) {
-    for (int j = tid; j < p.budget; j += kThreads) kept[j] = j < kv ? j : -1;
-    for (int64_t j = tid; j < p.w_ld; j += kThreads) wo[j] = j < kv ? w[j] : 0.f;
+    for (int j = me; j < p.budget; j += step) kept[j] = j < kv ? j : -1;
+    for (int j = me; j < p.w_ld; j += step) wo[j] = j < kv ? w[j] : 0.f;
     return;
   }
   const int lo = p.sink, hi = kv - p.recent;
+  // this CTA's keys, a run of whole rounds; the first round's stay in registers, four in a row a thread
+  const int rounds = (kv + kChunk * cluster - 1) / (kChunk * cluster);
+  const int per = rounds > 1 ? rounds * kChunk : (kv + cluster - 1) / cluster;
+  const int j_lo = min(kv, rank * per), j_hi = min(kv, j_lo + per);
+  float held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int j = j_lo + tid * kHeld + i;
+    held[i] = j < j_hi ? w[j] : 0.f;
+  }
+  // The weights of a round, thread by thread in order of their keys.
+  auto round_keys = [&](int r, auto&& use) {
+    const int j0 = j_lo + r * kChunk + tid * kHeld;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (j0 + i < j_hi) use(j0 + i, r == 0 ? held[i] : w[j0 + i], i);
+  };
   int need = p.budget - p.sink - p.recent;  // of the keys [lo, hi), hi - lo > need
+  const bool any = need > 0;
   uint32_t T = 0, mask = 0;
-  if (need > 0) {
+  if (any) {
+    for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
+    __syncthreads();
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kThreads) {
-        const uint32_t k = order_key(w[j]);
-        if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      int* h = hist[pass];
+      for (int r = 0; r < rounds; ++r)
+        round_keys(r, [&](int j, float x, int) {
+          const uint32_t k = order_key(x);
+          if (j >= lo && j < hi && (k & mask) == T) atomicAdd(&h[(k >> shift) & digit], 1);
+        });
+      cluster_barrier();
+      // the digit in which the need-th largest lies: bins from the top, two a thread
+      const int b0 = kBins - 1 - 2 * tid;
+      int c0 = 0, c1 = 0;
+      for (int q = 0; q < cluster; ++q) {
+        c0 += remote_int(&h[b0], q);
+        c1 += remote_int(&h[b0 - 1], q);
       }
-      __syncthreads();
-      // the digit in which the need-th largest lies: bins from the top
-      const int b0 = kBins - 1 - 2 * tid, c0 = hist[b0], c1 = hist[b0 - 1];
       int2 total;
       const int above = block_scan(make_int2(c0 + c1, 0), sh, total).x;
       if (above < need && above + c0 + c1 >= need) {
@@ -89,49 +131,62 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvict
       }
       __syncthreads();
       T |= uint32_t(found[0]) << shift;
-      mask |= ((1u << bits) - 1) << shift;
+      mask |= digit << shift;
       need = found[1];
       __syncthreads();
     }
   }
-  // keys in order, a block's width at a time
-  int2 before = make_int2(0, 0);  // kept for their place or above T; equal to T
-  const bool any = p.budget > p.sink + p.recent;
-  for (int j0 = 0; j0 < kv; j0 += kThreads) {
-    const int j = j0 + tid;
-    int2 c = make_int2(0, 0);
-    float x = 0.f;
-    if (j < kv) {
-      x = w[j];
-      if (j < lo || j >= hi) {
-        c.x = 1;
-      } else if (any) {
-        const uint32_t k = order_key(x);
-        c.x = k > T;
-        c.y = k == T;
-      }
-    }
-    int2 total;
-    const int2 at = block_scan(c, sh, total);
-    const int eq = before.y + at.y;
-    if (c.x || (c.y && eq < need)) {
-      const int i = before.x + at.x + (eq < need ? eq : need);
-      kept[i] = j;
-      wo[i] = x;
-    }
-    before.x += total.x;
-    before.y += total.y;
+  // each CTA's kept keys (for their place, or above T) and those equal to T, then their places
+  auto kind = [&](int j, float x) {
+    if (j < lo || j >= hi) return make_int2(1, 0);
+    const uint32_t k = order_key(x);
+    return any ? make_int2(k > T, k == T) : make_int2(0, 0);
+  };
+  int2 sum = make_int2(0, 0), total;
+  for (int r = 0; r < rounds; ++r)
+    round_keys(r, [&](int j, float x, int) {
+      const int2 c = kind(j, x);
+      sum.x += c.x, sum.y += c.y;
+    });
+  block_scan(sum, sh, total);
+  if (tid < 2) counts[tid] = tid == 0 ? total.x : total.y;
+  cluster_barrier();
+  int2 before = make_int2(0, 0);
+  for (int q = 0; q < rank; ++q) {
+    before.x += remote_int(&counts[0], q);
+    before.y += remote_int(&counts[1], q);
   }
-  for (int64_t j = p.budget + tid; j < p.w_ld; j += kThreads) wo[j] = 0.f;
+  for (int r = 0; r < rounds; ++r) {
+    int2 mine = make_int2(0, 0);
+    round_keys(r, [&](int j, float x, int) {
+      const int2 c = kind(j, x);
+      mine.x += c.x, mine.y += c.y;
+    });
+    int2 at = block_scan(mine, sh, total);
+    at.x += before.x, at.y += before.y;
+    round_keys(r, [&](int j, float x, int) {
+      const int2 c = kind(j, x);
+      if (c.x || (c.y && at.y < need)) {
+        const int i = at.x + min(at.y, need);
+        kept[i] = j;
+        wo[i] = x;
+      }
+      at.x += c.x, at.y += c.y;
+    });
+    before.x += total.x, before.y += total.y;
+  }
+  for (int j = p.budget + me; j < p.w_ld; j += step) wo[j] = 0.f;
+  cluster_barrier();  // the counts are read
 }
 
-// Rows [j0, j0 + 64) of the kept keys of one stream and key head per block.
+// Rows [j0, j0 + 32) of the kept keys of one stream and key head per block.
 __global__ void __launch_bounds__(kCopyThreads) paged_move_kernel(const PagedEvictParams p, int n_tiles) {
   __shared__ int64_t src[kCopyRows], dst[kCopyRows];
   __shared__ int own[kCopyRows];  // destination page of each row, or -1
   const int tid = threadIdx.x;
   const int chunks = p.row_bytes / 16;
   const long long items = (long long)p.s.n_seqs * p.kv_heads * n_tiles;
+  grid_dependency_wait();
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int tile = int(it % n_tiles), hk = int(it / n_tiles % p.kv_heads), b = int(it / n_tiles / p.kv_heads);
     const int kv = load_kv_len(p.s, b, p.err);
@@ -171,18 +226,19 @@ __global__ void __launch_bounds__(kCopyThreads) paged_move_kernel(const PagedEvi
       }
     }
     __syncthreads();
-    const char* in[2] = {static_cast<const char*>(p.k_pool), static_cast<const char*>(p.v_pool)};
-    char* out[2] = {static_cast<char*>(p.k_pool), static_cast<char*>(p.v_pool)};
     const int n = rows * chunks;
-    for (int x = 0; x < 2; ++x) {
 #pragma unroll 4
-      for (int i = tid; i < n; i += kCopyThreads) {
-        const int r = i / chunks, c = i - r * chunks;
-        if (dst[r] < 0) continue;
-        const uint4 v = src[r] < 0 ? make_uint4(0, 0, 0, 0)
-                                   : reinterpret_cast<const uint4*>(in[x] + src[r] * p.row_bytes)[c];
-        reinterpret_cast<uint4*>(out[x] + dst[r] * p.row_bytes)[c] = v;
+    for (int i = tid; i < n; i += kCopyThreads) {
+      const int r = i / chunks, c = i - r * chunks;
+      const int64_t from = src[r] * p.row_bytes, to = dst[r] * p.row_bytes;
+      if (to < 0) continue;
+      uint4 k = make_uint4(0, 0, 0, 0), v = k;
+      if (from >= 0) {
+        k = reinterpret_cast<const uint4*>(static_cast<const char*>(p.k_pool) + from)[c];
+        v = reinterpret_cast<const uint4*>(static_cast<const char*>(p.v_pool) + from)[c];
       }
+      reinterpret_cast<uint4*>(static_cast<char*>(p.k_pool) + to)[c] = k;
+      reinterpret_cast<uint4*>(static_cast<char*>(p.v_pool) + to)[c] = v;
     }
   }
 }
@@ -190,16 +246,31 @@ __global__ void __launch_bounds__(kCopyThreads) paged_move_kernel(const PagedEvi
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t st) {
-  paged_select_kernel<<<unsigned(p.s.n_seqs) * unsigned(p.kv_heads), kThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const unsigned items = unsigned(p.s.n_seqs) * unsigned(p.kv_heads);
+  // A cluster as large as the longest stream has rounds, up to 8 CTAs.
+  int cluster = 1;
+  while (cluster < kMaxCluster && cluster * kChunk < p.s.max_kv) cluster *= 2;
+  if ((long long)items * cluster >= (1LL << 31)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(items * unsigned(cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_select_kernel, p, cluster);
   if (e != cudaSuccess) return e;
   const int most = p.budget < p.s.max_kv ? p.budget : p.s.max_kv;
   const int n_tiles = (most + kCopyRows - 1) / kCopyRows;
-  const long long items = (long long)n_tiles * p.s.n_seqs * p.kv_heads;
-  if (items < 1) return cudaSuccess;
-  const long long cap = 64LL * sms;
-  paged_move_kernel<<<unsigned(items < cap ? items : cap), kCopyThreads, 0, st>>>(p, n_tiles);
-  return cudaGetLastError();
+  const long long moves = (long long)n_tiles * items, cap = 64LL * sms;
+  if (moves < 1) return cudaSuccess;
+  cfg.gridDim = dim3(unsigned(moves < cap ? moves : cap));
+  cfg.blockDim = dim3(kCopyThreads);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, paged_move_kernel, p, n_tiles);
 }
 
 }  // namespace arl2

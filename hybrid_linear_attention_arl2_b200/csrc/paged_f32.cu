@@ -13,7 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "paged.h"
-#include "paged_combine.cuh"
+#include "paged_join.cuh"
 #include "params.h"
 #include "sm100.cuh"
 
@@ -22,7 +22,9 @@ namespace arl2 {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
-using Plan = PagedPlan<1, kRows, kKeys>;
+using Plan = PagedPlan<1, kKeys>;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
@@ -38,7 +40,7 @@ __device__ __forceinline__ void load_keys(float* dst, int ld, const float* pool,
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (j < end) {
       const int pg = page_of(s, b, j, err);
-      if (pg >= 0) v = load4(pool + ((int64_t(pg) * kv_heads + hk) * s.page_size + j % s.page_size) * d + c);
+      if (pg >= 0) v = load4(pool + ((int64_t(pg) * kv_heads + hk) * s.page_size + s.page.mod(j)) * d + c);
     }
     store4(dst + r * ld + c, v);
   }
@@ -73,35 +75,40 @@ template <int DC>
 __global__ void __launch_bounds__(kThreads)
 paged_attn_f32_kernel(const PagedAttnParams p) {
   extern __shared__ float sm[];
-  __shared__ long long sh[64];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
   float* sQ = sm;
   float* sK = sQ + kRows * ld;
   float* sV = sK + kKeys * ld;
   float* sP = sV + kKeys * ld;  // [key][row], pitch 68
   constexpr int kPl = kRows + 4;
-  const PagedRange range = paged_range<Plan, kThreads>(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block, blockIdx.x,
-                                                       gridDim.x, p.err, sh);
-  if (tid < 2) p.rec[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
+  __shared__ PagedWalk<Plan> walk;
+  __shared__ int join, more;
+  if (tid < 32) {
+    PagedWalk<Plan> mine;
+    mine.find(p, blockIdx.x, gridDim.x);
+    if (tid == 0) {
+      walk = mine;
+      more = walk.next(p);
+    }
+  }
   __syncthreads();
   const float* q = static_cast<const float*>(p.q);
-  PagedWalk<Plan> walk(range, p.n_qblk);
-  while (walk.next(p.s, p.n_qblk, p.group, p.kv_heads, p.mask_block)) {
-    const PagedSeg<Plan>& s = walk.seg;
-    const int rows = s.blk.n_tok * p.group;
+  while (more) {
+    const PagedSeg<Plan> s = walk.seg;
+    const int rows = s.blk.n_tok * p.group, b = p.per_blk.div(s.f);
     // query rows, and each of this thread's rows' visible keys
     for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
       const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
-        v = load4(q + int64_t(s.blk.q0 + s.blk.t0 + r / p.group) * p.ld_q + (s.hk * p.group + r % p.group) * d + c);
+        v = load4(q + int64_t(s.blk.row0 + p.per_group.div(r)) * p.ld_q + (s.hk * p.group + p.per_group.mod(r)) * d + c);
       store4(sQ + r * ld + c, v);
     }
     int lim[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = 4 * ty + a;
-      lim[a] = r < rows ? visible_keys(s.blk.v, p.mask_block, s.blk.t0 + r / p.group) : 0;
+      lim[a] = r < rows ? visible_keys(s.blk.view(), p.mask, s.blk.t0 + p.per_group.div(r)) : 0;
     }
     float m[4], l[4], o[4][4 * DC];
 #pragma unroll
@@ -114,8 +121,8 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
     for (int j = s.u0; j < s.u1; ++j) {
       const int k0 = j * kKeys;
       __syncthreads();
-      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
-      load_keys(sV, ld, static_cast<const float*>(p.v_pool), p.s, s.b, s.hk, p.kv_heads, d, k0, s.blk.v.kv, p.err);
+      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, b, s.hk, p.kv_heads, d, k0, s.blk.kv, p.err);
+      load_keys(sV, ld, static_cast<const float*>(p.v_pool), p.s, b, s.hk, p.kv_heads, d, k0, s.blk.kv, p.err);
       __syncthreads();
       float acc[4][4];
       scores(sQ, sK, ld, d, ty, tx, acc);
@@ -171,13 +178,15 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
       }
     }
     const bool whole = s.whole();
-    const int piece = 2 * blockIdx.x + s.slot();
-    if (!whole && tid == 0) p.rec[piece] = make_int4(s.f, s.hk, s.starts(), s.ends());
+    const int piece = 2 * blockIdx.x + s.slot;
+    auto out_row = [&](int r) {
+      return int64_t(s.blk.row0 + p.per_group.div(r)) * p.heads + s.hk * p.group + p.per_group.mod(r);
+    };
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = 4 * ty + a;
       if (r >= rows) continue;
-      const int64_t orow = int64_t(s.blk.q0 + s.blk.t0 + r / p.group) * p.heads + s.hk * p.group + r % p.group;
+      const int64_t orow = out_row(r);
       const float inv = !whole ? 1.f : l[a] > 0.f ? 1.f / l[a] : 0.f;
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
@@ -197,7 +206,22 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
           p.lse[orow] = l[a] > 0.f ? (m[a] + log2f(l[a])) * 0.69314718055994531f : -INFINITY;
       }
     }
-    __syncthreads();  // sQ is read no more
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) join = last_piece(p.joined + 8 * s.owner, s.pieces);
+      __syncthreads();
+      if (join) {
+        const int r0 = (tid >> 5) * (kRows / (kThreads / 32));
+        join_rows<float, kRows>(p, s.owner, s.owner_slot, s.pieces, r0, min(rows - r0, kRows / (kThreads / 32)), out_row);
+      }
+    }
+    __syncthreads();  // sQ is read no more, nor the segment
+    if (tid == 0) {
+      walk.done(p);
+      more = walk.next(p);
+    }
+    __syncthreads();
   }
 }
 
@@ -227,7 +251,7 @@ paged_weights_f32_kernel(const PagedWeightParams p, int n_kt) {
       float w[4] = {0.f, 0.f, 0.f, 0.f};
       for (int t0 = 0; t0 < v.n; t0 += qt) {
         const int rows = min(qt, v.n - t0) * p.group;
-        if (visible_keys(v, p.mask_block, min(t0 + qt, v.n) - 1) <= k0) continue;  // no row of the tile sees the keys
+        if (visible_keys(v, p.mask, min(t0 + qt, v.n) - 1) <= k0) continue;  // no row of the tile sees the keys
         __syncthreads();
         for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
           const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
@@ -242,7 +266,7 @@ paged_weights_f32_kernel(const PagedWeightParams p, int n_kt) {
         for (int a = 0; a < 4; ++a) {
           const int r = 4 * ty + a;
           if (r >= rows) continue;
-          const int t = t0 + r / p.group, lim = visible_keys(v, p.mask_block, t);
+          const int t = t0 + r / p.group, lim = visible_keys(v, p.mask, t);
           const float lse = p.lse[int64_t(v.q0 + t) * p.heads + hk * p.group + r % p.group];
           if (lse == -INFINITY) continue;
 #pragma unroll
@@ -270,12 +294,8 @@ cudaError_t launch_attn(PagedAttnParams p, int grid, cudaStream_t st) {
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_f32_kernel<DC>),
                                    int(smem_floats(128) * sizeof(float)), &done);
   if (e != cudaSuccess) return e;
-  const int qt = kRows / p.group;
-  p.n_qblk = (p.s.max_q + qt - 1) / qt;
-  if ((long long)p.n_qblk * p.s.n_seqs >= (1LL << 31)) return cudaErrorInvalidValue;
   paged_attn_f32_kernel<DC><<<grid, kThreads, smem_floats(p.d) * sizeof(float), st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_combine<float, 1, kRows, kKeys>(p, grid, st);
+  return cudaGetLastError();
 }
 
 }  // namespace

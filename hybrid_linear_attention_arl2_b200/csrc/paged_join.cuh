@@ -1,0 +1,81 @@
+// Joins the pieces of an attention item that several CTAs share (paged.h's work
+// division), for the float32 and the bf16 kernel: with M the largest of their
+// maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in key order whoever
+// joins them.  The CTA that comes last does it, told by a count; nobody waits.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "paged.h"
+#include "sm100.cuh"
+
+namespace arl2 {
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// Whether the caller's piece is the last of `pieces`; what the others wrote is
+// visible to it then.  One thread calls it, after a fence by every writer.
+__device__ __forceinline__ bool last_piece(uint32_t* count, int pieces) {
+  if (atomicAdd(count, 1u) + 1u != uint32_t(pieces)) return false;
+  *count = 0;  // for the next launch
+  __threadfence();
+  return true;
+}
+
+// Rows [r0, r0 + n) of a piece's kPieceRows, n <= 32, by one warp: the lanes
+// hold the rows' statistics; then eight rows at a time, a lane's four columns
+// each.  `out(r)`: row r's index in O's [token, head] rows.
+template <typename T, int kPieceRows, class Out>
+__device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
+                                          const Out& out) {
+  const int lane = threadIdx.x & 31, d = p.d;
+  auto piece = [&](int k) { return int64_t(k == 0 ? 2 * owner + owner_slot : 2 * (owner + k)) * kPieceRows + r0; };
+  float M = -INFINITY, L = 0.f;
+  if (lane < n) {
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(&p.part_ml[piece(k) + lane].x));
+  }
+  if (M == -INFINITY) M = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float4 acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    L = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < pieces; ++k) {
+      const int64_t at = piece(k);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) ml = __ldcg(&p.part_ml[at + lane]);
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + i < n && lane * 4 < d)
+          v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (at + i0 + i) * d + lane * 4));
+      }
+      const float mine = exp2f(ml.x - M);
+      L = fmaf(ml.y, mine, L);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
+        acc[i] = make_float4(fmaf(v[i].x, w, acc[i].x), fmaf(v[i].y, w, acc[i].y), fmaf(v[i].z, w, acc[i].z),
+                             fmaf(v[i].w, w, acc[i].w));
+      }
+    }
+    const float rcp = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float inv = __shfl_sync(0xffffffffu, rcp, (i0 + i) & 31);
+      if (i0 + i < n && lane * 4 < d)
+        store4(static_cast<T*>(p.o) + out(r0 + i0 + i) * d + lane * 4,
+               make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+    }
+  }
+  if (lane < n && p.lse) p.lse[out(r0 + lane)] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace arl2

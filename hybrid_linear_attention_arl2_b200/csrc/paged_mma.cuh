@@ -96,16 +96,6 @@ __device__ __forceinline__ void store_sector(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// Keys per TMA box: boxes of a 128-key tile lie inside pages.
-__host__ __device__ __forceinline__ int box_keys(int page_size) {
-  int a = page_size, b = 128;
-  while (b) {
-    const int t = a % b;
-    a = b, b = t;
-  }
-  return a;
-}
-
 // The pool rows of a run of a stream's key tiles, fetched ahead: a warp's lanes
 // hold the boxes of 32 / boxes tiles in a row, and the page numbers of the ones
 // after them are on their way while these are used.  A box without a key, or
@@ -113,7 +103,8 @@ __host__ __device__ __forceinline__ int box_keys(int page_size) {
 // as zeros.
 struct BoxRows {
   const int32_t* table;
-  int box, boxes, per, kv, page_size, n_pages, hk, kv_heads;
+  FastDiv page;
+  int box, boxes, per, kv, n_pages, hk, kv_heads;
   int first, end;  // tiles held, [first, first + per); none from end on
   int row, ahead;  // this lane's box; the page number of its box `per` tiles on
   uint32_t* err;
@@ -124,14 +115,14 @@ struct BoxRows {
   }
   __device__ int fetch(int tile0) const {
     const int k = key_of(tile0);
-    return tile0 < end && k < kv ? table[k / page_size] : -1;
+    return tile0 < end && k < kv ? table[page.div(k)] : -1;
   }
   __device__ void turn(int tile0, int pg) {
     const int k = key_of(tile0);
-    row = n_pages * kv_heads * page_size;
+    row = n_pages * kv_heads * page.by;
     if (tile0 < end && k < kv) {
       if (unsigned(pg) < unsigned(n_pages))
-        row = (pg * kv_heads + hk) * page_size + k % page_size;
+        row = (pg * kv_heads + hk) * page.by + page.mod(k);
       else
         record_error(err, kDevPage);
     }
@@ -139,8 +130,8 @@ struct BoxRows {
   }
   // tiles [tile0, tile1) of stream b
   __device__ BoxRows(const PagedSeqs& s, int b, int kv_, int hk_, int kv_heads_, int tile0, int tile1, uint32_t* err_)
-      : table(s.pages + int64_t(b) * s.pages_ld), box(box_keys(s.page_size)), boxes(128 / box), per(32 / boxes), kv(kv_),
-        page_size(s.page_size), n_pages(s.n_pages), hk(hk_), kv_heads(kv_heads_), end(tile1), err(err_) {
+      : table(s.pages + int64_t(b) * s.pages_ld), page(s.page), box(s.box), boxes(s.boxes), per(s.per), kv(kv_),
+        n_pages(s.n_pages), hk(hk_), kv_heads(kv_heads_), end(tile1), err(err_) {
     const int pg = fetch(tile0);
     ahead = fetch(tile0 + per);
     turn(tile0, pg);

@@ -61,20 +61,22 @@ struct Stream {
     n_rt = some ? (v.n + qt - 1) / qt : 0;
   }
   // the first token that sees key j
-  __device__ int first_token(int mask_block, int j) const {
-    if (mask_block <= 0) return 0;
-    const long long past = (long long)j - (v.kv - v.n);
-    return past < mask_block ? 0 : int(past / mask_block * mask_block);
+  __device__ int first_token(const FastDiv& mask, int j) const {
+    if (mask.by <= 0) return 0;
+    const int past = j - (v.kv - v.n);
+    return past < mask.by ? 0 : past - mask.mod(past);
   }
-  __device__ int first_tile(int mask_block, int qt, int jt) const { return first_token(mask_block, jt * kKeys) / qt; }
-  __device__ long long units(int mask_block, int qt) const {
+  __device__ int first_tile(const PagedWeightParams& p, int jt) const {
+    return p.per_tile.div(first_token(p.mask, jt * kKeys));
+  }
+  __device__ long long units(const PagedWeightParams& p) const {
     if (n_kb == 0) return 0;
-    if (mask_block <= 0) return (long long)n_kb * n_rt;
-    const long long all = (long long)(v.kv - v.n) + mask_block;  // blocks that begin below it are seen by every tile
+    if (p.mask_block <= 0) return (long long)n_kb * n_rt;
+    const long long all = (long long)(v.kv - v.n) + p.mask_block;  // blocks that begin below it are seen by every tile
     long long full = all <= 0 ? 0 : (all + kKeys - 1) / kKeys;
     if (full > n_kb) full = n_kb;
     long long sum = full * n_rt;
-    for (int jt = int(full); jt < n_kb; ++jt) sum += n_rt - first_tile(mask_block, qt, jt);
+    for (int jt = int(full); jt < n_kb; ++jt) sum += n_rt - first_tile(p, jt);
     return sum;
   }
 };
@@ -108,13 +110,13 @@ struct Walk {
           } while (s.n_kb == 0);
         }
       }
-      u.rt = s.first_tile(p.mask_block, qt, u.jt);
+      u.rt = s.first_tile(p, u.jt);
       fresh = true;
       u.head = false;
     }
     --left;
     u.first = fresh;
-    if (fresh) u.starts = u.rt == s.first_tile(p.mask_block, qt, u.jt);
+    if (fresh) u.starts = u.rt == s.first_tile(p, u.jt);
     fresh = false;
     u.ends = u.rt == s.n_rt - 1;
     u.last = u.ends || left == 0;
@@ -149,7 +151,7 @@ __device__ __forceinline__ Walk find_range(const PagedWeightParams& p, int qt, l
   Walk w;
   w.left = 0, w.begun = false, w.fresh = true;
   auto cost = [&](int b, uint32_t* err) {
-    return b < p.s.n_seqs ? Stream(p.s, b, qt, err).units(p.mask_block, qt) * p.kv_heads : 0;
+    return b < p.s.n_seqs ? Stream(p.s, b, qt, err).units(p) * p.kv_heads : 0;
   };
   long long first = cost(tid, p.err), mine = first, total;
   for (int b = tid + kThreads; b < p.s.n_seqs; b += kThreads) mine += cost(b, p.err);
@@ -173,13 +175,13 @@ __device__ __forceinline__ Walk find_range(const PagedWeightParams& p, int qt, l
   }
   w.u.b = int(sh[24]);
   const Stream s(p.s, w.u.b, qt, nullptr);
-  const long long per = s.units(p.mask_block, qt);
+  const long long per = s.units(p);
   w.u.hk = int(sh[25] / per);
   const long long off = sh[25] % per;
   // the key block: a second search over the stream's blocks
   base = 0;
   for (int j0 = 0; j0 < s.n_kb; j0 += kThreads) {
-    const int jt = j0 + tid, r0 = jt < s.n_kb ? s.first_tile(p.mask_block, qt, jt) : 0;
+    const int jt = j0 + tid, r0 = jt < s.n_kb ? s.first_tile(p, jt) : 0;
     const long long c = jt < s.n_kb ? s.n_rt - r0 : 0;
     long long all;
     const long long beg = base + scan(c, sh, all);
@@ -293,7 +295,7 @@ __device__ __forceinline__ void lse_role(const PagedWeightParams& p, Walk walk, 
     float x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = lane + 32 * i, t = r / p.group;
+      const int r = lane + 32 * i, t = p.per_group.div(r);
       x[i] = -INFINITY;
       if (r < rows)
         x[i] = p.lse[int64_t(walk.s.v.q0 + u.rt * qt + t) * p.heads + u.hk * p.group + (r - t * p.group)];
@@ -357,7 +359,7 @@ __device__ __forceinline__ void sum_role(const PagedWeightParams& p, Walk walk, 
     }
     const int key = u.jt * kKeys + t * 128 + row, rows = walk.rows(p, qt);
     // the key is seen by the tile's columns [lo, rows)
-    const long long from = (long long)(walk.s.first_token(p.mask_block, key) - u.rt * qt) * p.group;
+    const long long from = (long long)(walk.s.first_token(p.mask, key) - u.rt * qt) * p.group;
     const int lo = from < 0 ? 0 : from > 128 ? 128 : int(from);
     const bool masked = __any_sync(0xffffffffu, lo > 0) || rows < 128;
     const uint32_t buf = g & 1;

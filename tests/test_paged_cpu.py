@@ -86,8 +86,7 @@ def test_foreign_paged_handles(lib):
 def test_wrapper_refusals():
     """The Python wrappers refuse tensors that the library would misread."""
     t = torch.zeros(6, 4, 8)
-    rows = {"q": 4, "k": 4}
-    ok = lambda **kw: arl2._token_rows(rows, 8, torch.float32, t.device, **kw)
+    ok = lambda **kw: arl2._token_rows(8, torch.float32, -1, [(name, x, 4) for name, x in kw.items()])
     wide = torch.zeros(6, 96)
     assert ok(q=t, k=t) == (0, 6)
     assert ok(q=wide[:, :32].unflatten(1, (4, 8)), k=wide[:, 32:64].unflatten(1, (4, 8))) == (96, 6)
