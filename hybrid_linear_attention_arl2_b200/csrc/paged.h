@@ -132,6 +132,33 @@ struct PrepParams {
   uint32_t* err;
 };
 
+// Launches with programmatic stream serialisation: the grid may be scheduled
+// while the kernel ahead of it on the stream finishes; every kernel launched so
+// waits for that kernel's completion (grid_dependency_wait) before it touches
+// global memory, in every thread, so that the stream's order is kept along any
+// chain of them.  cluster: CTAs of a cluster (0: none).
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+                              A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cudaStream_t st);
 // Attention: CTAs of the launch and rows of one of their pieces at most, which
 // size the handle's work space; then the launches.
@@ -216,6 +243,7 @@ struct PagedPlan {
     int n, kv;            // the stream's new tokens and cached keys
     __device__ SeqView view() const { return SeqView{0, n, kv}; }
   };
+
   __device__ static Block block(const PagedAttnParams& p, int f, uint32_t* err) {
     Block r;
     const int b = p.per_blk.div(f);
@@ -262,16 +290,17 @@ struct PagedWalk {
 
   // Finds the CTA's range; called by one warp.  Two passes over the blocks of
   // rows: their total, then the one that holds the range's first unit.
-  __device__ __forceinline__ void find(const PagedAttnParams& p, int cta, int grid) {
+  __device__ void find(const PagedAttnParams& p, int cta, int grid) {
     const int lane = threadIdx.x & 31, F = p.s.n_seqs * p.n_qblk;
     typename Plan::Block blk;
     blk.units = 0;
     int total = 0, mine = 0;
+#pragma unroll 1
     for (int f = lane; f < F; f += 32) {
       blk = Plan::block(p, f, cta == 0 ? p.err : nullptr);
       mine += blk.units;
     }
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = __reduce_add_sync(0xffffffffu, mine);
     total = mine * p.kv_heads;
     const int ctas = min(total, grid);
     left = 0;
@@ -282,6 +311,7 @@ struct PagedWalk {
     pos = begin(cta);
     left = begin(cta + 1) - pos;
     int before = 0;
+#pragma unroll 1
     for (int f0 = 0; f0 < F; f0 += 32) {
       if (F > 32) {
         blk.units = 0;
@@ -289,6 +319,7 @@ struct PagedWalk {
       }
       const int c = f0 + lane < F ? blk.units * p.kv_heads : 0;
       int inc = c;
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;

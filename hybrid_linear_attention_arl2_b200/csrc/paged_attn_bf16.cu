@@ -536,6 +536,7 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // (the window begins on 1024 bytes; a layout that does not fit is refused)
   if (size_t(smem - smem_raw) + kLayout > size_t(kSmem)) {
+    grid_dependency_wait();
     if (threadIdx.x == 0) record_error(p.err, kDevBadShape);
     return;
   }
@@ -561,6 +562,8 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
   }
+  grid_dependency_wait();
+  allow_dependent_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -632,8 +635,7 @@ cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, con
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
-  paged_attn_bf16_kernel<<<grid, kThreads, kSmem, st>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  return launch_overlapped(paged_attn_bf16_kernel, dim3(unsigned(grid)), kThreads, kSmem, st, 0, tq, tk, tv, p);
 }
 
 }  // namespace arl2

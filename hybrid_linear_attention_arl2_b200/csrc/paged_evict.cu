@@ -67,6 +67,8 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvict
   __shared__ int counts[2];
   const int item = blockIdx.x / cluster, rank = blockIdx.x - item * cluster, tid = threadIdx.x;
   const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int kv = load_kv_len(p.s, b, p.err);
   if (kv < 0) return;  // (the whole cluster)
   const int64_t row = int64_t(b) * p.kv_heads + hk;
@@ -187,6 +189,7 @@ __global__ void __launch_bounds__(kCopyThreads) paged_move_kernel(const PagedEvi
   const int chunks = p.row_bytes / 16;
   const long long items = (long long)p.s.n_seqs * p.kv_heads * n_tiles;
   grid_dependency_wait();
+  allow_dependent_launch();
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int tile = int(it % n_tiles), hk = int(it / n_tiles % p.kv_heads), b = int(it / n_tiles / p.kv_heads);
     const int kv = load_kv_len(p.s, b, p.err);
@@ -251,26 +254,14 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t 
   int cluster = 1;
   while (cluster < kMaxCluster && cluster * kChunk < p.s.max_kv) cluster *= 2;
   if ((long long)items * cluster >= (1LL << 31)) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(items * unsigned(cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_select_kernel, p, cluster);
+  const cudaError_t e = launch_overlapped(paged_select_kernel, dim3(items * unsigned(cluster)), kThreads, 0, st, cluster, p,
+                                          cluster);
   if (e != cudaSuccess) return e;
   const int most = p.budget < p.s.max_kv ? p.budget : p.s.max_kv;
   const int n_tiles = (most + kCopyRows - 1) / kCopyRows;
   const long long moves = (long long)n_tiles * items, cap = 64LL * sms;
   if (moves < 1) return cudaSuccess;
-  cfg.gridDim = dim3(unsigned(moves < cap ? moves : cap));
-  cfg.blockDim = dim3(kCopyThreads);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, paged_move_kernel, p, n_tiles);
+  return launch_overlapped(paged_move_kernel, dim3(unsigned(moves < cap ? moves : cap)), kCopyThreads, 0, st, 0, p, n_tiles);
 }
 
 }  // namespace arl2

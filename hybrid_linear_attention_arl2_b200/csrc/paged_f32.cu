@@ -74,6 +74,8 @@ __host__ __device__ inline size_t smem_floats(int d) {
 template <int DC>
 __global__ void __launch_bounds__(kThreads)
 paged_attn_f32_kernel(const PagedAttnParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   extern __shared__ float sm[];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
   float* sQ = sm;
@@ -230,6 +232,8 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
 // tiles of 64, a thread sums its 4 rows' weights of its 4 keys.
 __global__ void __launch_bounds__(kThreads)
 paged_weights_f32_kernel(const PagedWeightParams p, int n_kt) {
+  grid_dependency_wait();
+  allow_dependent_launch();
   extern __shared__ float sm[];
   __shared__ float part[16][kKeys];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
@@ -294,8 +298,8 @@ cudaError_t launch_attn(PagedAttnParams p, int grid, cudaStream_t st) {
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_f32_kernel<DC>),
                                    int(smem_floats(128) * sizeof(float)), &done);
   if (e != cudaSuccess) return e;
-  paged_attn_f32_kernel<DC><<<grid, kThreads, smem_floats(p.d) * sizeof(float), st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(paged_attn_f32_kernel<DC>, dim3(unsigned(grid)), kThreads, smem_floats(p.d) * sizeof(float), st, 0,
+                           p);
 }
 
 }  // namespace
@@ -313,8 +317,7 @@ cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st
   const long long n_kt = (p.w_ld + kKeys - 1) / kKeys;
   const long long items = n_kt * p.s.n_seqs * p.kv_heads;
   const unsigned grid = unsigned(items < (1 << 20) ? items : (1 << 20));
-  paged_weights_f32_kernel<<<grid, kThreads, bytes, st>>>(p, int(n_kt));
-  return cudaGetLastError();
+  return launch_overlapped(paged_weights_f32_kernel, dim3(grid), kThreads, size_t(bytes), st, 0, p, int(n_kt));
 }
 
 }  // namespace arl2

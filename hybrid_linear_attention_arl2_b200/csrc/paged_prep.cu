@@ -59,6 +59,8 @@ prep_kernel(const __grid_constant__ PrepParams p, int tpb) {
   constexpr int N = Vec<T>::N, kGroups = kThreads / LPR, kUnroll = 2;
   __shared__ float2 turn[kMaxTokens][64];  // (cos, sin)
   __shared__ int2 dst[kMaxTokens];         // append: stream's page (or -1) and row in it
+  grid_dependency_wait();
+  allow_dependent_launch();
   const int tid = threadIdx.x, lane = tid % LPR, group = tid / LPR;
   const int64_t t0 = int64_t(blockIdx.x) * tpb;
   const int nt = int(min(int64_t(tpb), p.tokens - t0));
@@ -205,11 +207,8 @@ prep_kernel(const __grid_constant__ PrepParams p, int tpb) {
 }
 
 template <typename T, int LPR>
-void launch(const PrepParams& p, bool append, dim3 grid, int tpb, cudaStream_t st) {
-  if (append)
-    prep_kernel<T, LPR, true><<<grid, kThreads, 0, st>>>(p, tpb);
-  else
-    prep_kernel<T, LPR, false><<<grid, kThreads, 0, st>>>(p, tpb);
+cudaError_t launch(const PrepParams& p, bool append, dim3 grid, int tpb, cudaStream_t st) {
+  return launch_overlapped(append ? prep_kernel<T, LPR, true> : prep_kernel<T, LPR, false>, grid, kThreads, 0, st, 0, p, tpb);
 }
 
 }  // namespace
@@ -232,23 +231,22 @@ cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cu
   const dim3 grid{unsigned(x), unsigned(y)};
   if (dtype == ARL2_BF16) {
     switch (lpr) {
-      case 1: launch<__nv_bfloat16, 1>(p, append, grid, tpb, st); break;
-      case 2: launch<__nv_bfloat16, 2>(p, append, grid, tpb, st); break;
-      case 4: launch<__nv_bfloat16, 4>(p, append, grid, tpb, st); break;
-      case 8: launch<__nv_bfloat16, 8>(p, append, grid, tpb, st); break;
-      default: launch<__nv_bfloat16, 16>(p, append, grid, tpb, st); break;
+      case 1: return launch<__nv_bfloat16, 1>(p, append, grid, tpb, st);
+      case 2: return launch<__nv_bfloat16, 2>(p, append, grid, tpb, st);
+      case 4: return launch<__nv_bfloat16, 4>(p, append, grid, tpb, st);
+      case 8: return launch<__nv_bfloat16, 8>(p, append, grid, tpb, st);
+      default: return launch<__nv_bfloat16, 16>(p, append, grid, tpb, st);
     }
   } else {
     switch (lpr) {
-      case 1: launch<float, 1>(p, append, grid, tpb, st); break;
-      case 2: launch<float, 2>(p, append, grid, tpb, st); break;
-      case 4: launch<float, 4>(p, append, grid, tpb, st); break;
-      case 8: launch<float, 8>(p, append, grid, tpb, st); break;
-      case 16: launch<float, 16>(p, append, grid, tpb, st); break;
-      default: launch<float, 32>(p, append, grid, tpb, st); break;
+      case 1: return launch<float, 1>(p, append, grid, tpb, st);
+      case 2: return launch<float, 2>(p, append, grid, tpb, st);
+      case 4: return launch<float, 4>(p, append, grid, tpb, st);
+      case 8: return launch<float, 8>(p, append, grid, tpb, st);
+      case 16: return launch<float, 16>(p, append, grid, tpb, st);
+      default: return launch<float, 32>(p, append, grid, tpb, st);
     }
   }
-  return cudaGetLastError();
 }
 
 }  // namespace arl2

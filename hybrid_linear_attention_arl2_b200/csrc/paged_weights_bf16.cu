@@ -423,6 +423,7 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // (the window begins on 1024 bytes; a layout that does not fit is refused)
   if (size_t(smem - smem_raw) + kLayout > size_t(kSmem)) {
+    grid_dependency_wait();
     if (threadIdx.x == 0) record_error(p.err, kDevBadShape);
     return;
   }
@@ -445,6 +446,8 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
     tma_prefetch(&tm_q);
     tma_prefetch(&tm_k);
   }
+  grid_dependency_wait();
+  allow_dependent_launch();
   if (threadIdx.x < 2) p.rec[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
   const Walk walk = find_range(p, qt, reinterpret_cast<long long*>(sL));
   tc_fence_before();
@@ -491,6 +494,7 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
 constexpr int kTail = 4096;
 __global__ void __launch_bounds__(kKeys) paged_weights_finish_kernel(const PagedWeightParams p, int ctas) {
   grid_dependency_wait();
+  allow_dependent_launch();
   const int tid = threadIdx.x;
   if (int(blockIdx.x) < ctas) {
     const int c = blockIdx.x;
@@ -540,20 +544,12 @@ cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensor
     CUtensorMap tq;
     if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
     ctas = sms;
-    paged_weights_bf16_kernel<<<ctas, kThreads, kSmem, st>>>(tq, tk, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_overlapped(paged_weights_bf16_kernel, dim3(unsigned(ctas)), kThreads, kSmem, st, 0, tq, tk, p);
+    if (e != cudaSuccess) return e;
   }
   const long long items = (p.w_ld + kTail - 1) / kTail * p.s.n_seqs * p.kv_heads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas + (items < 65536 ? items : 65536)));
-  cfg.blockDim = dim3(kKeys);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_weights_finish_kernel, p, ctas);
+  return launch_overlapped(paged_weights_finish_kernel, dim3(unsigned(ctas + (items < 65536 ? items : 65536))), kKeys, 0, st,
+                           0, p, ctas);
 }
 
 }  // namespace arl2
