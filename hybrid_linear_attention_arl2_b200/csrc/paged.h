@@ -124,7 +124,7 @@ struct PrepParams {
   int32_t heads, kv_heads, d;
   int32_t n_axes, axis_dim[3], halves, rot;  // rot = R, 0: no rotation
   int32_t norm;
-  float eps;
+  float eps, inv_d;            // inv_d = 1 / d
   uint64_t freq[64];           // 2^64 theta^(-2 i / n) / (2 pi) of each pair
   // append
   PagedSeqs s;

@@ -262,6 +262,7 @@ arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t h
   p.heads = heads;
   p.kv_heads = kv_heads;
   p.d = head_dim;
+  p.inv_d = 1.f / float(head_dim);
   PAGED_TRY(launch_prep(p, dtype, false, sms, static_cast<cudaStream_t>(stream)));
   return ARL2_OK;
 }
@@ -384,6 +385,7 @@ arl2_status arl2_paged_append(arl2_paged_t h, const arl2_paged_batch* batch, con
   p.heads = c.heads;
   p.kv_heads = c.kv_heads;
   p.d = c.head_dim;
+  p.inv_d = 1.f / float(c.head_dim);
   p.s = seqs_of(h, batch);
   p.k_pool = h->k_pool;
   p.v_pool = h->v_pool;

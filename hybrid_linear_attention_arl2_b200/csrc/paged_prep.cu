@@ -3,14 +3,16 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * w;   (y0, y1) -> (y0 cos a - y1 sin a, y0 sin a + y1 cos a)
 //
-// A row (one token, one head) is held by a group of lanes, 16 bytes a lane:
-// the sum of squares is a few shuffles, pairs of neighbours lie in one lane and
-// pairs R/2 apart in two (one shuffle a channel).  The angles of a token are
-// the same for all its heads: the block computes them once, one thread a pair,
-// while its first rows are on their way.  An angle is pos * freq with freq a
-// 64-bit fraction of a turn: the product modulo 2^64 is the fraction of the
-// turn exactly up to pos * 2^-65, so no position loses bits to range reduction;
-// its upper 32 bits go to sincospif.  Bound: bytes (each row in and out once).
+// A group of lanes takes a token, 16 bytes of a row a lane, and goes through
+// its rows (heads of Q, K and, appending, V), six in flight: the sum of squares
+// is a few shuffles, pairs of neighbours lie in one lane and pairs R/2 apart in
+// two (one shuffle a channel).  The angles are the token's: a block computes
+// them once, a thread a pair, and a lane keeps those of its channels.
+// An angle is pos * freq with freq a 64-bit fraction of a turn: the product
+// modulo 2^64 is the fraction of the turn exactly up to pos * 2^-65, so no
+// position loses bits to range reduction; its upper 32 bits go to sincospif.
+// Few tokens: a token's rows are split over several groups, so that every SM
+// has loads in flight.  Bound: bytes (each row in and out once).
 
 #include <cuda_bf16.h>
 
@@ -21,8 +23,8 @@ namespace arl2 {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens of a block at most
+constexpr int kThreads = 128;
+constexpr int kAhead = 6;  // rows in flight of a group
 
 template <typename T>
 struct Vec {  // 16 bytes of a row
@@ -50,165 +52,166 @@ __device__ __forceinline__ uint4 pack(const Vec<__nv_bfloat16>& x) {
                     pack_bf16x2(x.v[6], x.v[7]));
 }
 
-// LPR: lanes of a row (a power of two >= d * sizeof(T) / 16).  A block takes
-// `tpb` tokens; blockIdx.y takes rows y, y + gridDim.y, ... of them in steps of
-// the block's row groups, which spreads few tokens over more SMs.
+// LPR: lanes of a row (a power of two >= d * sizeof(T) / 16).  A token's rows
+// are split over `parts` groups of LPR lanes.
 template <typename T, int LPR, bool kAppend>
 __global__ void __launch_bounds__(kThreads)
-prep_kernel(const __grid_constant__ PrepParams p, int tpb) {
-  constexpr int N = Vec<T>::N, kGroups = kThreads / LPR, kUnroll = 2;
-  __shared__ float2 turn[kMaxTokens][64];  // (cos, sin)
-  __shared__ int2 dst[kMaxTokens];         // append: stream's page (or -1) and row in it
+prep_kernel(const __grid_constant__ PrepParams p, int parts) {
+  constexpr int N = Vec<T>::N;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int tid = threadIdx.x, lane = tid % LPR, group = tid / LPR;
-  const int64_t t0 = int64_t(blockIdx.x) * tpb;
-  const int nt = int(min(int64_t(tpb), p.tokens - t0));
-  const int H = p.heads, Hk = p.kv_heads, nq = p.q_out ? H : 0;
-  const int per_tok = nq + Hk + (kAppend ? Hk : 0), rows = nt * per_tok;
-  const bool on = lane * N < p.d;
-  const int step = kGroups * int(gridDim.y);
-
-  auto src = [&](int r) -> const uint4* {
-    const int t = r / per_tok, i = r - t * per_tok;
-    const T* base = i < nq        ? static_cast<const T*>(p.q) + (t0 + t) * p.ld_q + int64_t(i) * p.d
-                    : i < nq + Hk ? static_cast<const T*>(p.k) + (t0 + t) * p.ld_k + int64_t(i - nq) * p.d
-                                  : static_cast<const T*>(p.v) + (t0 + t) * p.ld_v + int64_t(i - nq - Hk) * p.d;
-    return reinterpret_cast<const uint4*>(base) + lane;
-  };
-  int r = int(blockIdx.y) * kGroups + group;
-  uint4 in[kUnroll];
+  // groups of a block: kThreads / LPR, `parts` (a power of two) to a token
+  constexpr int kGroups = kThreads / LPR;
+  __shared__ float2 turn[kThreads * N / 2];  // (cos, sin) of the block's tokens' pairs
+  const int lane = threadIdx.x % LPR, c = lane * N, group = threadIdx.x / LPR;
+  const int tokens = kGroups / parts, mine = group / parts, part = group - mine * parts;
+  const int64_t t0 = int64_t(blockIdx.x) * tokens;
+  const bool have = t0 + mine < p.tokens, on = have && c < p.d;
+  const int64_t t = have ? t0 + mine : p.tokens - 1;  // (a group without a token keeps step with its warp)
+  const int row4 = p.d / N;  // 16-byte words of a row
+  // Rows part + r0, part + r0 + parts, ... of n, kAhead of them.
+  auto fetch = [&](uint4 (&x)[kAhead], const T* src, int n, int r0) {
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) in[u] = on && r + u * step < rows ? *src(r + u * step) : make_uint4(0, 0, 0, 0);
-  Vec<T> wq, wk;
-  if (p.norm && on) {
-    unpack(reinterpret_cast<const uint4*>(p.w_q)[lane], wq);
-    unpack(reinterpret_cast<const uint4*>(p.w_k)[lane], wk);
-  }
-  // the block's angles
-  const int pairs = p.rot / 2;
-  for (int i = tid; i < nt * pairs; i += kThreads) {
-    const int t = i / pairs, pr = i - t * pairs;
-    const int e0 = p.axis_dim[0] >> 1, e1 = e0 + (p.n_axes > 1 ? p.axis_dim[1] >> 1 : 0);
-    const int axis = pr < e0 ? 0 : pr < e1 ? 1 : 2;
-    const int pos = p.pos[(t0 + t) * p.n_axes + axis];
-    const uint64_t turns = uint64_t(int64_t(pos)) * p.freq[pr];
-    float sn, cs;
-    sincospif(float(int(turns >> 32)) * (1.f / 2147483648.f), &sn, &cs);  // pi * (turns * 2^-63)
-    turn[t][pr] = make_float2(cs, sn);
-  }
-  if (kAppend) {
-    // A token's stream: the number of streams that end at or before it.
-    int b[kMaxTokens];
-#pragma unroll
-    for (int t = 0; t < kMaxTokens; ++t) b[t] = 0;
-    for (int s0 = 0; s0 < p.s.n_seqs; s0 += kThreads) {
-      const int e = s0 + tid < p.s.n_seqs ? p.s.q_start[s0 + tid + 1] : 0x7fffffff;
-#pragma unroll
-      for (int t = 0; t < kMaxTokens; ++t) b[t] += __syncthreads_count(int64_t(e) <= t0 + t);
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + part + i * parts;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (on && r < n) x[i] = reinterpret_cast<const uint4*>(src)[r * row4 + lane];
     }
-    if (tid < nt) {
-      int bt = 0;
+  };
+  const T* q = static_cast<const T*>(p.q) + t * p.ld_q;
+  const T* k = static_cast<const T*>(p.k) + t * p.ld_k;
+  const int nq = p.q_out ? p.heads : 0;
+  uint4 first_q[kAhead], first_k[kAhead];
+  fetch(first_q, q, nq, 0);
+  fetch(first_k, k, p.kv_heads, 0);
+  // the block's angles, a thread a pair; then each lane takes those of its channels
+  const int half = p.rot / 2;
+  const bool in_rot = c < p.rot, lo = c < half;
+  float cs[N], sn[N];
+  if (half > 0) {
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+      const int j = i / half, pr = i - j * half;
+      const int e0 = p.axis_dim[0] >> 1, e1 = e0 + (p.axis_dim[1] >> 1);
+      if (t0 + j < p.tokens) {
+        const int pos = p.pos[(t0 + j) * p.n_axes + (pr < e0 ? 0 : pr < e1 ? 1 : 2)];
+        const uint64_t turns = uint64_t(int64_t(pos)) * p.freq[pr];
+        float2 a;
+        sincospif(float(int(turns >> 32)) * (1.f / 2147483648.f), &a.y, &a.x);  // pi * (turns * 2^-63)
+        turn[i] = a;
+      }
+    }
+    __syncthreads();
 #pragma unroll
-      for (int t = 0; t < kMaxTokens; ++t)
-        if (tid == t) bt = b[t];
-      int2 d2 = make_int2(-2, 0);  // no stream's token: nothing of it is written
-      if (bt < p.s.n_seqs) {
-        const SeqView v = load_seq(p.s, bt, p.err);
-        const int64_t t = t0 + tid - v.q0;
-        if (v.n >= 0 && t >= 0 && t < v.n) {
-          const int64_t j = int64_t(v.kv) - v.n + t;
-          d2.x = -1;  // its Q is written, its K and V have no row
-          if (j >= 0) {
-            const int pg = page_of(p.s, bt, int(j), p.err);
-            if (pg >= 0) d2 = make_int2(pg, int(j) % p.s.page_size);
-          } else {
-            record_error(p.err, kDevPage);
-          }
+    for (int e = 0; e < N; ++e) {
+      if (!p.halves && (e & 1)) continue;
+      const int pr = p.halves ? (lo ? c + e : c - half + e) : (c + e) >> 1;
+      const float2 a = (p.halves ? in_rot : c + e < p.rot) && have ? turn[mine * half + pr] : make_float2(1.f, 0.f);
+      cs[e] = a.x, sn[e] = a.y;
+    }
+  }
+  // append: the row of the token's K and V in the pools
+  int64_t dst = -1;
+  bool used = true;  // the token belongs to a stream
+  if (kAppend) {
+    // its stream: as many as end at or before it come first
+    int b = 0;
+    const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (threadIdx.x % 32 / LPR * LPR);
+    for (int s0 = 0; s0 < p.s.n_seqs; s0 += LPR) {
+      const bool before = s0 + lane < p.s.n_seqs && p.s.q_start[s0 + lane + 1] <= t;
+      b += __popc(__ballot_sync(0xffffffffu, before) & mask);
+    }
+    used = b < p.s.n_seqs;
+    if (used) {
+      const SeqView sv = load_seq(p.s, b, lane == 0 ? p.err : nullptr);
+      const int64_t i = t - sv.q0;
+      used = sv.n >= 0 && i >= 0 && i < sv.n;
+      if (used) {
+        const int64_t j = int64_t(sv.kv) - sv.n + i;
+        if (j >= 0) {
+          const int pg = page_of(p.s, b, int(j), lane == 0 ? p.err : nullptr);
+          if (pg >= 0) dst = int64_t(pg) * p.kv_heads * p.s.page_size + p.s.page.mod(int(j));
+        } else if (lane == 0) {
+          record_error(p.err, kDevPage);
         }
       }
-      dst[tid] = d2;
     }
   }
-  __syncthreads();
-
-  for (; __any_sync(0xffffffffu, r < rows); r += kUnroll * step) {  // (whole warps leave together)
-    uint4 cur[kUnroll];
+  const bool part_rot = p.rot < p.d;
+  const int other = in_rot ? (lo ? lane + half / N : lane - half / N) : lane;  // (halves; half is a multiple of N)
+  // Norm and rotation of n rows, as many rounds in every group.
+  auto turned = [&](uint4 (&x)[kAhead], const void* weights, const T* src, int n, T* out, int pitch, bool write) {
+    Vec<T> w;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      cur[u] = in[u];
-      const int rn = r + (kUnroll + u) * step;
-      if (on && rn < rows) in[u] = *src(rn);
-    }
+    for (int e = 0; e < N; ++e) w.v[e] = 1.f;
+    if (p.norm && c < p.d) unpack(reinterpret_cast<const uint4*>(weights)[lane], w);
+    for (int r0 = 0; r0 < n; r0 += kAhead * parts) {
+      if (r0 > 0) fetch(x, src, n, r0);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int ru = r + u * step;
-      const bool live = ru < rows;
-      const int t = live ? ru / per_tok : 0, i = live ? ru - t * per_tok : 0;
-      const bool is_q = i < nq, is_v = i >= nq + Hk;
-      Vec<T> x;
-      unpack(cur[u], x);
-      if (p.norm) {
-        float ss = 0.f;
+      for (int i = 0; i < kAhead; ++i) {
+        if (r0 + i * parts >= n) continue;  // (no group has one)
+        const int r = r0 + part + i * parts;
+        Vec<T> y;
+        unpack(x[i], y);
+        if (p.norm) {
+          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss = fmaf(x.v[e], x.v[e], ss);
+          for (int e = 0; e < N; e += 2) s2 = __ffma2_rn(make_float2(y.v[e], y.v[e + 1]), make_float2(y.v[e], y.v[e + 1]), s2);
+          float ss = s2.x + s2.y;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss / float(p.d) + p.eps);
-#pragma unroll
-        for (int e = 0; e < N; ++e) x.v[e] = is_v ? x.v[e] : x.v[e] * inv * (is_q ? wq.v[e] : wk.v[e]);
-      }
-      if (p.rot > 0) {
-        const int c = lane * N, half = p.rot / 2;
-        if (p.halves) {
-          // the partner holds channels half before or after; half is a multiple of N
-          const bool lo = c < half, in_rot = c < p.rot;
-          const int other = in_rot ? (lo ? lane + half / N : lane - half / N) : lane;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float y = __shfl_sync(0xffffffffu, x.v[e], other, LPR);
-            if (in_rot && !is_v) {
-              const float2 a = turn[t][lo ? c + e : c - half + e];
-              x.v[e] = lo ? x.v[e] * a.x - y * a.y : y * a.y + x.v[e] * a.x;
-            }
-          }
-        } else if (!is_v) {
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
 #pragma unroll
           for (int e = 0; e < N; e += 2) {
-            if (c + e < p.rot) {
-              const float2 a = turn[t][(c + e) >> 1];
-              const float y0 = x.v[e], y1 = x.v[e + 1];
-              x.v[e] = y0 * a.x - y1 * a.y;
-              x.v[e + 1] = y0 * a.y + y1 * a.x;
-            }
+            const float2 m = __fmul2_rn(make_float2(w.v[e], w.v[e + 1]), make_float2(inv, inv));
+            const float2 z = __fmul2_rn(make_float2(y.v[e], y.v[e + 1]), m);
+            y.v[e] = z.x, y.v[e + 1] = z.y;
           }
         }
-      }
-      if (!live || !on) continue;
-      T* out;
-      if (kAppend) {
-        const int2 d2 = dst[t];
-        if (is_q) {
-          if (d2.x == -2) continue;
-          out = static_cast<T*>(p.q_out) + (t0 + t) * p.ld_qo + int64_t(i) * p.d;
-        } else {
-          if (d2.x < 0) continue;
-          const int hk = is_v ? i - nq - Hk : i - nq;
-          out = static_cast<T*>(is_v ? p.v_pool : p.k_pool) +
-                ((int64_t(d2.x) * Hk + hk) * p.s.page_size + d2.y) * p.d;
+        if (p.halves && half > 0) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float z = __shfl_sync(0xffffffffu, y.v[e], other, LPR);
+            if (in_rot) y.v[e] = lo ? y.v[e] * cs[e] - z * sn[e] : z * sn[e] + y.v[e] * cs[e];
+          }
+        } else if (half > 0) {
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            if (part_rot && c + e >= p.rot) continue;
+            const float2 z = __fmul2_rn(make_float2(y.v[e + 1], y.v[e]), make_float2(-sn[e], sn[e]));
+            const float2 o = __ffma2_rn(make_float2(y.v[e], y.v[e + 1]), make_float2(cs[e], cs[e]), z);
+            y.v[e] = o.x, y.v[e + 1] = o.y;
+          }
         }
-      } else {
-        out = is_q ? static_cast<T*>(p.q_out) + (t0 + t) * p.ld_qo + int64_t(i) * p.d
-                   : static_cast<T*>(p.k_out) + (t0 + t) * p.ld_ko + int64_t(i - nq) * p.d;
+        if (write && on && r < n) reinterpret_cast<uint4*>(out + int64_t(r) * pitch)[lane] = pack(y);
       }
-      reinterpret_cast<uint4*>(out)[lane] = is_v ? cur[u] : pack(x);
+    }
+  };
+  if (kAppend) {  // V as it is
+    const T* v = static_cast<const T*>(p.v) + t * p.ld_v;
+    T* out = static_cast<T*>(p.v_pool) + dst * p.d;
+    const int64_t pitch = int64_t(p.s.page_size) * p.d;
+    for (int r0 = 0; r0 < p.kv_heads; r0 += kAhead * parts) {
+      uint4 x[kAhead];
+      fetch(x, v, p.kv_heads, r0);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int r = r0 + part + i * parts;
+        if (dst >= 0 && on && r < p.kv_heads) reinterpret_cast<uint4*>(out + r * pitch)[lane] = x[i];
+      }
     }
   }
+  if (nq > 0) turned(first_q, p.w_q, q, nq, static_cast<T*>(p.q_out) + t * p.ld_qo, p.d, used);
+  if (kAppend)
+    turned(first_k, p.w_k, k, p.kv_heads, static_cast<T*>(p.k_pool) + dst * p.d, p.s.page_size * p.d, dst >= 0);
+  else
+    turned(first_k, p.w_k, k, p.kv_heads, static_cast<T*>(p.k_out) + t * p.ld_ko, p.d, true);
 }
 
 template <typename T, int LPR>
-cudaError_t launch(const PrepParams& p, bool append, dim3 grid, int tpb, cudaStream_t st) {
-  return launch_overlapped(append ? prep_kernel<T, LPR, true> : prep_kernel<T, LPR, false>, grid, kThreads, 0, st, 0, p, tpb);
+cudaError_t launch(const PrepParams& p, bool append, int parts, cudaStream_t st) {
+  const int64_t tokens = kThreads / LPR / parts;  // of a block
+  const dim3 grid{unsigned((p.tokens + tokens - 1) / tokens)};
+  return launch_overlapped(append ? prep_kernel<T, LPR, true> : prep_kernel<T, LPR, false>, grid, kThreads, 0, st, 0, p, parts);
 }
 
 }  // namespace
@@ -218,33 +221,27 @@ cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cu
   const int chunks = p.d * (dtype == ARL2_BF16 ? 2 : 4) / 16;
   int lpr = 1;
   while (lpr < chunks) lpr *= 2;
-  const int groups = kThreads / lpr, per_tok = (p.q_out ? p.heads : 0) + p.kv_heads * (append ? 2 : 1);
-  // Few tokens: one a block, its rows spread over blocks.  Many: four a block,
-  // whose rows keep loads in flight while the angles are computed once.
-  const int tpb = p.tokens >= 4LL * sms ? kMaxTokens : 1;
-  int y = 1;
-  if (p.tokens < sms) {
-    y = (per_tok + groups - 1) / groups;
-    if (y > 64) y = 64;
-  }
-  const int64_t x = (p.tokens + tpb - 1) / tpb;
-  const dim3 grid{unsigned(x), unsigned(y)};
+  // Parts, a power of two up to a block's groups, until an SM has 256 threads:
+  // a single token's rows go to all of a block's groups, 27000 tokens take one.
+  const int groups = kThreads / lpr;
+  int parts = 1;
+  while (parts < groups && p.tokens * parts * lpr < int64_t(sms) * 256) parts *= 2;
   if (dtype == ARL2_BF16) {
     switch (lpr) {
-      case 1: return launch<__nv_bfloat16, 1>(p, append, grid, tpb, st);
-      case 2: return launch<__nv_bfloat16, 2>(p, append, grid, tpb, st);
-      case 4: return launch<__nv_bfloat16, 4>(p, append, grid, tpb, st);
-      case 8: return launch<__nv_bfloat16, 8>(p, append, grid, tpb, st);
-      default: return launch<__nv_bfloat16, 16>(p, append, grid, tpb, st);
+      case 1: return launch<__nv_bfloat16, 1>(p, append, parts, st);
+      case 2: return launch<__nv_bfloat16, 2>(p, append, parts, st);
+      case 4: return launch<__nv_bfloat16, 4>(p, append, parts, st);
+      case 8: return launch<__nv_bfloat16, 8>(p, append, parts, st);
+      default: return launch<__nv_bfloat16, 16>(p, append, parts, st);
     }
   } else {
     switch (lpr) {
-      case 1: return launch<float, 1>(p, append, grid, tpb, st);
-      case 2: return launch<float, 2>(p, append, grid, tpb, st);
-      case 4: return launch<float, 4>(p, append, grid, tpb, st);
-      case 8: return launch<float, 8>(p, append, grid, tpb, st);
-      case 16: return launch<float, 16>(p, append, grid, tpb, st);
-      default: return launch<float, 32>(p, append, grid, tpb, st);
+      case 1: return launch<float, 1>(p, append, parts, st);
+      case 2: return launch<float, 2>(p, append, parts, st);
+      case 4: return launch<float, 4>(p, append, parts, st);
+      case 8: return launch<float, 8>(p, append, parts, st);
+      case 16: return launch<float, 16>(p, append, parts, st);
+      default: return launch<float, 32>(p, append, parts, st);
     }
   }
 }
