@@ -228,14 +228,16 @@ __device__ __forceinline__ int visible_keys(const SeqView& v, const FastDiv& mas
 // in units: with two tiles one unit is one tile of kKeys keys against both; a
 // block of one tile (single tokens) splits its keys between the two halves of
 // the CTA, so a unit is two key tiles.  Items lie in a row, f first and key heads
-// within it, and the CTAs take equal contiguous ranges of the units (no CTA has
-// more than one unit more than another, however ragged the batch is).  An item
+// within it, and the CTAs take equal contiguous ranges of the cost, kItemCost +
+// units an item (its start, end and output take as long as that many units), so
+// that ragged batches are spread as evenly as one long stream.  An item
 // cut by a range's end is finished from the CTAs' pieces by the one that comes
 // last: a CTA has at most two, one at its range's begin (slot 0) and one at its
 // end (slot 1).  An item has at least one unit, so that rows which see no key get
 // their zeros.  (The launch bounds the units below 2^31.)
-template <int kTiles, int kKeys>
+template <int kTiles, int kKeys, int kItemCost_>
 struct PagedPlan {
+  static constexpr int kItemCost = kItemCost_;
   struct Block {
     int row0, t0, n_tok;  // first token row, its token in the stream, tokens (0: no item)
     int tiles;            // 1 or 2
@@ -277,19 +279,22 @@ struct PagedSeg {
 
 template <class Plan>
 struct PagedWalk {
-  int each, more;  // units of every range; the first `more` have one more
-  int pos, left;   // unit that comes next, units of the range that are left
+  int each, more;  // cost of every range; the first `more` have one more
+  int at, end;     // cost before the current item, and where the range ends
   bool have, fresh;
   PagedSeg<Plan> seg;
 
   __device__ int begin(int cta) const { return each * cta + min(cta, more); }
-  __device__ int owner(int unit) const {  // the CTA whose range holds a unit
+  __device__ int owner(int cost) const {  // the CTA whose range holds it
     const int big = (each + 1) * more;
-    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+    return cost < big ? cost / (each + 1) : more + (cost - big) / each;
+  }
+  __device__ static int cost_of(const typename Plan::Block& blk, int kv_heads) {
+    return blk.units > 0 ? (blk.units + Plan::kItemCost) * kv_heads : 0;
   }
 
   // Finds the CTA's range; called by one warp.  Two passes over the blocks of
-  // rows: their total, then the one that holds the range's first unit.
+  // rows: their total, then the one that holds the range's begin.
   __device__ void find(const PagedAttnParams& p, int cta, int grid) {
     const int lane = threadIdx.x & 31, F = p.s.n_seqs * p.n_qblk;
     typename Plan::Block blk;
@@ -298,18 +303,16 @@ struct PagedWalk {
 #pragma unroll 1
     for (int f = lane; f < F; f += 32) {
       blk = Plan::block(p, f, cta == 0 ? p.err : nullptr);
-      mine += blk.units;
+      mine += cost_of(blk, p.kv_heads);
     }
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    total = mine * p.kv_heads;
+    total = __reduce_add_sync(0xffffffffu, mine);
     const int ctas = min(total, grid);
-    left = 0;
+    at = end = 0;
     have = fresh = true;
     if (cta >= ctas) return;
     each = total / ctas;
     more = total - each * ctas;
-    pos = begin(cta);
-    left = begin(cta + 1) - pos;
+    const int pos = begin(cta);
     int before = 0;
 #pragma unroll 1
     for (int f0 = 0; f0 < F; f0 += 32) {
@@ -317,7 +320,7 @@ struct PagedWalk {
         blk.units = 0;
         if (f0 + lane < F) blk = Plan::block(p, f0 + lane, nullptr);
       }
-      const int c = f0 + lane < F ? blk.units * p.kv_heads : 0;
+      const int c = f0 + lane < F ? cost_of(blk, p.kv_heads) : 0;
       int inc = c;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
@@ -328,50 +331,56 @@ struct PagedWalk {
       const unsigned hit = __ballot_sync(0xffffffffu, off >= 0 && off < c);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        const int at = __shfl_sync(0xffffffffu, off, src);
+        const int in = __shfl_sync(0xffffffffu, off, src);
         int* w = reinterpret_cast<int*>(&blk);
         for (int i = 0; i < int(sizeof(blk) / 4); ++i) w[i] = __shfl_sync(0xffffffffu, w[i], src);
         seg.blk = blk;
         seg.f = f0 + src;
-        seg.hk = at / blk.units;
-        seg.u1 = at - seg.hk * blk.units;  // (the next segment begins at u1)
+        seg.hk = in / (blk.units + Plan::kItemCost);
+        const int inner = in - seg.hk * (blk.units + Plan::kItemCost);
+        at = pos - inner;
+        seg.u1 = max(0, inner - Plan::kItemCost);  // (the next segment begins at u1)
+        end = begin(cta + 1);
         return;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    left = 0;  // (cannot happen: the range lies inside the items)
   }
 
+  // The next segment with units; a range may end or begin in an item's kItemCost.
   __device__ bool next(const PagedAttnParams& p) {
-    if (left <= 0) return false;
-    if (!have) {
-      const int F = p.s.n_seqs * p.n_qblk;
-      do {
-        if (++seg.f >= F) return false;  // (cannot happen)
-        seg.blk = Plan::block(p, seg.f, nullptr);
-      } while (seg.blk.units == 0);
-      seg.hk = 0;
-      have = true;
+    while (at < end) {
+      if (!have) {
+        const int F = p.s.n_seqs * p.n_qblk;
+        do {
+          if (++seg.f >= F) return false;  // (cannot happen: the range lies inside the items)
+          seg.blk = Plan::block(p, seg.f, nullptr);
+        } while (seg.blk.units == 0);
+        seg.hk = 0;
+        have = true;
+      }
+      seg.u0 = seg.u1;
+      seg.u1 = min(seg.blk.units, end - at - Plan::kItemCost);
+      if (seg.u1 <= seg.u0) return false;  // (the range ends before the item's first unit)
+      seg.slot = fresh ? 0 : 1;
+      seg.owner = 0, seg.pieces = 1, seg.owner_slot = 0;
+      if (seg.u1 - seg.u0 < seg.blk.units) {
+        seg.owner = owner(at + Plan::kItemCost);
+        seg.pieces = owner(at + Plan::kItemCost + seg.blk.units - 1) - seg.owner + 1;
+        seg.owner_slot = begin(seg.owner) >= at ? 0 : 1;
+      }
+      fresh = false;
+      return true;
     }
-    seg.u0 = seg.u1;
-    const int take = min(seg.blk.units - seg.u0, left);
-    seg.u1 = seg.u0 + take;
-    seg.slot = fresh ? 0 : 1;
-    seg.owner = 0, seg.pieces = 1, seg.owner_slot = 0;
-    if (take < seg.blk.units) {
-      const int item = pos - seg.u0;
-      seg.owner = owner(item);
-      seg.pieces = owner(item + seg.blk.units - 1) - seg.owner + 1;
-      seg.owner_slot = begin(seg.owner) == item ? 0 : 1;
-    }
-    fresh = false;
-    pos += take;
-    left -= take;
-    return true;
+    return false;
   }
   // After a segment's use: moves on to the next item where this one ended.
   __device__ void done(const PagedAttnParams& p) {
-    if (seg.u1 < seg.blk.units) return;
+    if (seg.u1 < seg.blk.units) {
+      at = end;
+      return;
+    }
+    at += seg.blk.units + Plan::kItemCost;
     seg.u1 = 0;
     if (++seg.hk == p.kv_heads) have = false;
   }
@@ -385,7 +394,7 @@ inline bool paged_plan(PagedAttnParams& p, int tile_rows, int tiles, int keys) {
   const int64_t tokens = int64_t(p.qt) * tiles;
   const int64_t n_qblk = (p.s.max_q + tokens - 1) / tokens;
   if (n_qblk * p.s.n_seqs >= (int64_t(1) << 30)) return false;
-  if (double(n_qblk) * p.s.n_seqs * (p.s.max_kv / keys + 1) * p.kv_heads >= 2147483647.0) return false;
+  if (double(n_qblk) * p.s.n_seqs * (p.s.max_kv / keys + 8) * p.kv_heads >= 2147483647.0) return false;
   p.n_qblk = int32_t(n_qblk);
   p.mask = FastDiv(p.mask_block);
   p.per_group = FastDiv(p.group);

@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRing = 5, kSegs = 4;
-using Plan = PagedPlan<2, 128>;
+using Plan = PagedPlan<2, 128, 2>;
 
 enum {
   B_QF = 0,              // Q tiles loaded (bytes)
@@ -355,6 +355,64 @@ __device__ __forceinline__ float exp_chunk(const uint32_t* r, const float2 sc, c
   return sa.x + sa.y;
 }
 
+// 32 columns of an output row.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&o)[32], bool sectors) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      v[x] = pack_bf16x2(__uint_as_float(o[c * 16 + 2 * x]), __uint_as_float(o[c * 16 + 2 * x + 1]));
+    if (sectors) {
+      store_sector(dst + c * 16, v);
+    } else {
+      reinterpret_cast<uint4*>(dst + c * 16)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<uint4*>(dst + c * 16)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+// Joins the pieces of a thread's own row (see join_rows).
+__device__ __forceinline__ void join_own(const PagedAttnParams& p, const Seg& s, int row, int64_t orow, bool sectors) {
+  auto first = [&](int k) { return int64_t(k == 0 ? 2 * s.owner + s.owner_slot : 2 * (s.owner + k)) * 256; };
+  float M = -INFINITY, L = 0.f;
+  for (int k = 0; k < s.pieces; ++k) M = fmaxf(M, __ldcg(&p.part_ml[first(k) + row].x));
+  if (M == -INFINITY) M = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    float acc[32];
+#pragma unroll
+    for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+    L = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < s.pieces; ++k) {
+      const float2 ml = __ldcg(&p.part_ml[first(k) + row]);
+      float4 v[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + piece_at(first(k), row, q * 4 + c));
+        v[2 * c] = __ldcg(src);
+        v[2 * c + 1] = __ldcg(src + 1);
+      }
+      const float w = exp2f(ml.x - M);
+      L = fmaf(ml.y, w, L);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        acc[4 * x] = fmaf(v[x].x, w, acc[4 * x]);
+        acc[4 * x + 1] = fmaf(v[x].y, w, acc[4 * x + 1]);
+        acc[4 * x + 2] = fmaf(v[x].z, w, acc[4 * x + 2]);
+        acc[4 * x + 3] = fmaf(v[x].w, w, acc[4 * x + 3]);
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t o[32];
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(acc[x] * inv);
+    store_row32(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32, o, sectors);
+  }
+  if (p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
 // Warpgroup t: tile t's rows, one a thread, 64 keys a step.
 __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader segs, uint64_t* bars, float* stats,
                                              uint32_t tmem, int t, const WaitCtl& w) {
@@ -468,7 +526,9 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
     const int tok_row = s->row0 + (s->dual ? t * p.qt : 0), head0 = s->hk * p.group;
     auto out_row = [&](int r) { return int64_t(tok_row + p.per_group.div(r)) * p.heads + head0 + p.per_group.mod(r); };
     const int64_t orow = out_row(row);
-    const int64_t prow = int64_t(2 * blockIdx.x + s->slot) * 256 + t * 128 + row;
+    const int64_t piece = int64_t(2 * blockIdx.x + s->slot) * 256;
+    const int64_t prow = piece + t * 128 + row;
+    const bool sectors = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
     if (warp_live) {
       // 32 columns at a time in a loop of its own: code that runs once costs its fetch
 #pragma unroll 1
@@ -485,19 +545,12 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
         }
         if (!live) continue;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              v[x] = pack_bf16x2(__uint_as_float(o[c * 8 + 2 * x]), __uint_as_float(o[c * 8 + 2 * x + 1]));
-            dst[c] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+          store_row32(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32, o, sectors);
         } else {
-          float* dst = p.part_o + prow * 128 + q * 32;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) store_sector(dst + c * 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[c * 8]));
+          for (int c = 0; c < 4; ++c)
+            store_sector(p.part_o + piece_at(piece, t * 128 + row, q * 4 + c),
+                         *reinterpret_cast<const uint32_t(*)[8]>(&o[c * 8]));
         }
       }
       if (live) {
@@ -511,9 +564,14 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
         __syncwarp();
         int last = 0;
         if (lane == 0) last = last_piece(p.joined + 8 * s->owner + 4 * t + quarter, s->pieces);
-        if (__shfl_sync(0xffffffffu, last, 0))
-          join_rows<__nv_bfloat16, 256>(p, s->owner, s->owner_slot, s->pieces, t * 128 + quarter * 32,
-                                        min(32, rows - quarter * 32), [&](int r) { return out_row(r - t * 128); });
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          const int n = min(32, rows - quarter * 32);
+          if (n <= 8)  // few rows, and often many pieces: the warp goes through them together
+            join_rows<__nv_bfloat16, 256, true>(p, s->owner, s->owner_slot, s->pieces, t * 128 + quarter * 32, n,
+                                                [&](int r) { return out_row(r - t * 128); });
+          else if (live)
+            join_own(p, *s, t * 128 + row, orow, sectors);
+        }
       }
     }
     if (join) {  // O_1 and its statistics are read

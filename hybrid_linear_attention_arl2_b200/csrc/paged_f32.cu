@@ -22,7 +22,7 @@ namespace arl2 {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
-using Plan = PagedPlan<1, kKeys>;
+using Plan = PagedPlan<1, kKeys, 1>;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -215,7 +215,7 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
       __syncthreads();
       if (join) {
         const int r0 = (tid >> 5) * (kRows / (kThreads / 32));
-        join_rows<float, kRows>(p, s.owner, s.owner_slot, s.pieces, r0, min(rows - r0, kRows / (kThreads / 32)), out_row);
+        join_rows<float, kRows, false>(p, s.owner, s.owner_slot, s.pieces, r0, min(rows - r0, kRows / (kThreads / 32)), out_row);
       }
     }
     __syncthreads();  // sQ is read no more, nor the segment

@@ -25,10 +25,19 @@ __device__ __forceinline__ bool last_piece(uint32_t* count, int pieces) {
   return true;
 }
 
+// Where eight columns (32 bytes) of a row of a 256-row piece of 128 columns
+// lie, in floats: the rows of a warp side by side, so that a thread that holds
+// a row stores and loads full lines with its warp.  `first`: the piece's first
+// row among all pieces' rows.
+__device__ __forceinline__ int64_t piece_at(int64_t first, int row, int col8) {
+  return first * 128 + (col8 * 256 + row) * 8;
+}
+
 // Rows [r0, r0 + n) of a piece's kPieceRows, n <= 32, by one warp: the lanes
 // hold the rows' statistics; then eight rows at a time, a lane's four columns
-// each.  `out(r)`: row r's index in O's [token, head] rows.
-template <typename T, int kPieceRows, class Out>
+// each.  `out(r)`: row r's index in O's [token, head] rows.  kLanes: the piece
+// is laid out for a thread a row (piece_at), else row by row.
+template <typename T, int kPieceRows, bool kLanes, class Out>
 __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
                                           const Out& out) {
   const int lane = threadIdx.x & 31, d = p.d;
@@ -55,7 +64,8 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, i
       for (int i = 0; i < 8; ++i) {
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + i < n && lane * 4 < d)
-          v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (at + i0 + i) * d + lane * 4));
+          v[i] = __ldcg(reinterpret_cast<const float4*>(
+              p.part_o + (kLanes ? piece_at(at - r0, r0 + i0 + i, lane >> 1) + (lane & 1) * 4 : (at + i0 + i) * d + lane * 4)));
       }
       const float mine = exp2f(ml.x - M);
       L = fmaf(ml.y, mine, L);
