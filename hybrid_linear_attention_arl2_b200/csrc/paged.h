@@ -41,12 +41,12 @@ struct PagedSeqs {
   int32_t n_seqs, tokens, max_q, max_kv, pages_ld;
   int32_t page_size, n_pages;
   FastDiv page;            // by page_size
-  int32_t box, boxes, per;  // keys of a TMA box, boxes of a 128-key tile, tiles that 32 boxes make (bf16)
+  int32_t box;             // keys of a TMA box (bf16)
 };
 
-// Keys per TMA box: the boxes of a 128-key tile lie inside pages.
+// Keys per TMA box: the boxes of a 64-key tile lie inside pages.
 inline int box_keys(int page_size) {
-  int a = page_size, b = 128;
+  int a = page_size, b = 64;
   while (b) {
     const int t = a % b;
     a = b, b = t;

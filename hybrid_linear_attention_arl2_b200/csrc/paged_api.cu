@@ -185,8 +185,6 @@ PagedSeqs seqs_of(const arl2_paged* h, const arl2_paged_batch* b) {
   s.n_pages = h->cfg.n_pages;
   s.page = h->page;
   s.box = h->box;
-  s.boxes = 128 / h->box;
-  s.per = 32 / s.boxes;
   return s;
 }
 

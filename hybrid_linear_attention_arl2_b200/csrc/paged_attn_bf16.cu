@@ -6,22 +6,21 @@
 // key head) are the pairs (token, head of the group), so the heads that share
 // keys share their tile: a tile is 128 rows.  Two tiles are in flight, a softmax
 // warpgroup each.  A block with one tile (single tokens, a chunk's tail) takes
-// two key tiles at once instead: both halves hold the same queries, half t the
-// key tiles 2 u + t, and their (m, l, O) are joined at the end, so that a single
-// row keeps as many bytes in flight as 256 rows do.
+// two key tiles at once instead: both halves hold the same queries, half t every
+// second tile of 64 keys, and their (m, l, O) are joined at the end, so that a
+// single row keeps as many bytes in flight as 256 rows do.
 //
 // A half's work goes in steps of 64 keys with two S in tensor memory, so that
 // S(i + 1) is there when the softmax of step i ends: S(i) = Q K^T (128 x 64,
 // fp32), P(i) over it in place (bf16 pairs), O += P(i) V.  With 128 keys a step
 // and one S a half each half waited for its own products (softmax 2800 clocks,
 // products and signals 1500, one after the other); the halves hid too little of
-// each other.  Order of products, which the loader's ring of 32 KB tiles (128
-// keys) follows:  S_0(0) S_1(0) S_0(1) S_1(1), then for each step i
-//   PV_0(i) S_0(i + 2) PV_1(i) S_1(i + 2).
-// S(i + 2) overwrites P(i) behind PV(i) in the pipe.
+// each other.  Order of a half's products:  S(0) S(1), then for each step i
+// PV(i) S(i + 2);  the loader's ring of 16 KB tiles follows it.  S(i + 2)
+// overwrites P(i) behind PV(i) in the pipe.
 //
 // Warps: 0 loads (Q by one box a tile, K and V by boxes inside pages, one lane a
-// box, page numbers fetched ahead), 1 issues the products, 2 describes the
+// box, page numbers fetched ahead), 1 and 3 issue the products, 2 describes the
 // segments, 4-7 and 8-11 softmax, O's rescaling (only when a row's maximum grows
 // by more than 8 in log2 units: P <= 256) and the output; a thread has one row.
 // Tensor memory: S_t, P_t of step i at t 128 + (i & 1) 64; O_t at 256 + t 128.
@@ -40,12 +39,14 @@ namespace arl2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRing = 5, kSegs = 4;
+constexpr int kRing = 10, kSegs = 4;
+constexpr int kStepKeys = 64;
+constexpr uint32_t kSlot = kStepKeys * 256;  // a step's K or V: two boxes of 64 columns
 using Plan = PagedPlan<2, 128, 2>;
 
 enum {
   B_QF = 0,              // Q tiles loaded (bytes)
-  B_QE,                  // Q read by the segment's last S (commit)
+  B_QE,                  // Q read by the segment's last S (commit, both issuers)
   B_SF,                  // [t][2] S_t of a step in tensor memory (commit)
   B_PF = B_SF + 4,       // [t][2] P_t of a step written (the warpgroup's 4 warps)
   B_PD = B_PF + 4,       // [t] a step's product with V done (commit)
@@ -53,14 +54,14 @@ enum {
   B_MG = B_OF + 2,       // half 1's statistics in shared memory (4 warps)
   B_MD,                  // half 1's O and statistics read by half 0 (4 warps)
   B_RF,                  // [kRing] ring slot loaded (bytes)
-  B_RE = B_RF + kRing,   // [kRing] ring slot read (commit)
+  B_RE = B_RF + kRing,   // [kRing] ring slot read (two commits)
   B_GF = B_RE + kRing,   // [kSegs] segment described
-  B_GE = B_GF + kSegs,   // [kSegs] description read (loader, issuer, 8 softmax warps)
+  B_GE = B_GF + kSegs,   // [kSegs] description read (the V loader, both issuers, 8 softmax warps)
   B_DRAIN = B_GE + kSegs,
   B_COUNT
 };
 
-// A segment as the roles need it, written by one warp into a ring.
+// A segment as the roles need it, written by the K loader into a ring.
 struct Seg {
   int more;            // 0: the CTA's range is done
   int b, hk;           // stream, key head
@@ -68,8 +69,8 @@ struct Seg {
   int tok0;            // its token within the stream's new ones
   int n_new, kv;       // the stream's new tokens and cached keys
   int dual;            // two tiles of rows on the same key tiles; else one tile on alternate ones
-  int n[2];            // units each half takes part in
-  int j0;              // first key tile (dual: of both; else of half 0, half 1's is the next)
+  int n[2];            // steps of 64 keys of each half
+  int j0;              // first step's tile of 64 keys (dual: of both; else of half 0, half 1's is the next)
   int rows[2];         // rows of each half's tile
   int slot;            // of this CTA's piece, and the pieces of the item (PagedSeg)
   int owner, pieces, owner_slot;
@@ -83,18 +84,20 @@ __device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, const 
   g.tok0 = s.blk.t0;
   g.n_new = s.blk.n, g.kv = s.blk.kv;
   g.dual = s.blk.tiles == 2;
-  g.j0 = g.dual ? s.u0 : 2 * s.u0;
-  // the block's last token sees its key tiles; with two tiles the first may see fewer
-  const int all = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + s.blk.n_tok - 1) + 127) >> 7;
+  // the block's last token sees all its key tiles; with two row tiles the first may see fewer
+  const int all = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + s.blk.n_tok - 1) + kStepKeys - 1) / kStepKeys;
   if (g.dual) {
-    const int nk = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + qt - 1) + 127) >> 7;
-    g.n[0] = max(0, min(nk, s.u1) - s.u0);
-    g.n[1] = max(0, min(all, s.u1) - s.u0);
+    const int nk = (visible_keys(s.blk.view(), p.mask, s.blk.t0 + qt - 1) + kStepKeys - 1) / kStepKeys;
+    g.j0 = 2 * s.u0;
+    g.n[0] = max(0, min(nk, 2 * s.u1) - g.j0);
+    g.n[1] = max(0, min(all, 2 * s.u1) - g.j0);
     g.rows[0] = qt * p.group;
     g.rows[1] = (s.blk.n_tok - qt) * p.group;
   } else {
-    g.n[0] = max(0, min((all + 1) >> 1, s.u1) - s.u0);
-    g.n[1] = max(0, min(all >> 1, s.u1) - s.u0);
+    g.j0 = 4 * s.u0;
+    const int n = max(0, min(all, 4 * s.u1) - g.j0);
+    g.n[0] = (n + 1) >> 1;
+    g.n[1] = n >> 1;
     g.rows[0] = g.rows[1] = s.blk.n_tok * p.group;
   }
   g.slot = s.slot;
@@ -118,221 +121,221 @@ struct SegReader {
   }
 };
 
-__device__ __forceinline__ void seg_role(const PagedAttnParams& p, uint64_t* bars, Seg* ring, const WaitCtl& w) {
+// ------------------------------------------------------------------ loads
+// Two warps, one for K (which also describes the segments and loads Q) and one
+// for V, so that neither's waits and page numbers hold up the other: one warp
+// took 600 clocks a tile, where the products want one every 450.  K and V tiles
+// lie in the ring in the order in which the products take them: the first steps'
+// K (one tile a step in a dual segment, two otherwise, two steps), then V(y),
+// K(y + first).  Each warp waits for its own tiles' slots alone: its last tile
+// lies at most five places back, and both issuers release all tiles in order, so
+// a slot it asks for is at most one fill behind.
+struct Loader {
+  const PagedAttnParams& p;
+  uint64_t* bars;
+  uint8_t* sR;
+  const CUtensorMap* tm;
+  const WaitCtl& w;
+  uint32_t slot = 0, round = 0;
+  __device__ void skip() {
+    if (++slot == kRing) slot = 0, ++round;
+  }
+  __device__ __forceinline__ bool load(BoxRows<kStepKeys>& rows, int tile) {
+    if (round > 0 && !warp_wait(&bars[B_RE + slot], (round - 1) & 1, w)) return false;
+    if ((threadIdx.x & 31) == 0) mbar_expect_tx(&bars[B_RF + slot], kSlot);
+    __syncwarp();
+    rows.load(tile, sR + slot * kSlot, tm, &bars[B_RF + slot]);
+    skip();
+    return true;
+  }
+  // This warp's tiles of a segment.
+  __device__ __forceinline__ bool segment(const Seg& s, bool is_v) {
+    const int n = s.dual ? s.n[1] : s.n[0] + s.n[1], first = s.dual ? 2 : 4, j0 = s.j0;
+    BoxRows<kStepKeys> rows(p.s, s.b, s.kv, s.hk, p.kv_heads, j0, j0 + n, p.err);
+    for (int i = -first; i < n; ++i) {
+      if (i >= 0) {
+        if (!is_v)
+          skip();
+        else if (!load(rows, j0 + i))
+          return false;
+      }
+      if (i + first < n) {
+        if (is_v)
+          skip();
+        else if (!load(rows, j0 + i + first))
+          return false;
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void k_role(const PagedAttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                                       uint64_t* bars, Seg* ring, uint8_t* sQ, uint8_t* sR, const WaitCtl& w) {
+  const int lane = threadIdx.x & 31, qt = p.qt;
   PagedWalk<Plan> walk;
   walk.find(p, blockIdx.x, gridDim.x);
-  if ((threadIdx.x & 31) != 0) return;
-  bool more = true;
-  for (uint32_t k = 0; more; ++k) {
-    more = walk.next(p);
-    if (k >= kSegs && !mbar_wait(&bars[B_GE + k % kSegs], (k / kSegs - 1) & 1, w)) return;
-    Seg& g = ring[k % kSegs];
-    if (more) {
-      describe(g, walk.seg, p);
-      walk.done(p);
-    } else {
-      g.more = 0;
-    }
-    mbar_arrive(&bars[B_GF + k % kSegs]);
-  }
-}
-
-// ------------------------------------------------------------------ loads
-__device__ __forceinline__ void load_role(const PagedAttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                                          const CUtensorMap* tm_v, SegReader segs, uint64_t* bars, uint8_t* sQ,
-                                          uint8_t* sR, const WaitCtl& w) {
-  const int lane = threadIdx.x & 31;
-  const int qt = p.qt;
-  uint32_t ring = 0, k = 0;
-  for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
-    const bool dual = s->dual;
-    if (s->n[0] == 0 && s->n[1] == 0) continue;
-    if (k > 0 && !warp_wait(&bars[B_QE], (k - 1) & 1, w)) return;
+  Loader loader{p, bars, sR, tm_k, w};
+  uint32_t q_loads = 0;
+  for (uint32_t k = 0;; ++k) {
+    const bool more = walk.next(p);
+    if (k >= kSegs && !warp_wait(&bars[B_GE + k % kSegs], (k / kSegs - 1) & 1, w)) return;
+    Seg& s = ring[k % kSegs];
     if (lane == 0) {
-      const int tiles = dual ? 2 : 1;
+      if (more)
+        describe(s, walk.seg, p);
+      else
+        s.more = 0;
+      mbar_arrive(&bars[B_GF + k % kSegs]);
+    }
+    __syncwarp();
+    if (!more) return;
+    walk.done(p);
+    if (s.n[0] == 0 && s.n[1] == 0) continue;
+    if (q_loads > 0 && !warp_wait(&bars[B_QE], (q_loads - 1) & 1, w)) return;
+    ++q_loads;
+    if (lane == 0) {
+      const int tiles = s.dual ? 2 : 1;
       mbar_expect_tx(&bars[B_QF], 2u * uint32_t(tiles) * uint32_t(qt * p.group) * 128u);
       for (int t = 0; t < tiles; ++t)
         for (int h = 0; h < 2; ++h)
-          tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s->hk * p.group, s->row0 + t * qt);
+          tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s.hk * p.group, s.row0 + t * qt);
     }
-    // K and V tiles in the order in which the products take them: a dual
-    // segment's K(u), V(u); else K(0), K(1), V(0), K(2), V(1), ... of its tiles
-    const int n = dual ? s->n[1] : s->n[0] + s->n[1], lag = dual ? 0 : 1, j0 = s->j0;
-    BoxRows rk(p.s, s->b, s->kv, s->hk, p.kv_heads, j0, j0 + n, p.err), rv = rk;
-    auto load = [&](BoxRows& rows, int i, const CUtensorMap* tm) {
-      const uint32_t slot = ring % kRing;
-      if (ring >= kRing && !warp_wait(&bars[B_RE + slot], ((ring / kRing) - 1) & 1, w)) return false;
-      if (lane == 0) mbar_expect_tx(&bars[B_RF + slot], kTile);
-      __syncwarp();
-      rows.load(j0 + i, sR + slot * kTile, tm, &bars[B_RF + slot]);
-      __syncwarp();
-      ++ring;
-      return true;
-    };
-    for (int i = 0; i < n + lag; ++i) {
-      if (i < n && !load(rk, i, tm_k)) return;
-      if (i >= lag && !load(rv, i - lag, tm_v)) return;
-    }
-    ++k;
+    __syncwarp();
+    if (!loader.segment(s, false)) return;
   }
+}
+
+__device__ __forceinline__ void v_role(const PagedAttnParams& p, const CUtensorMap* tm_v, SegReader segs, uint64_t* bars,
+                                       uint8_t* sR, const WaitCtl& w) {
+  Loader loader{p, bars, sR, tm_v, w};
+  for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w))
+    if (s->n[0] + s->n[1] > 0 && !loader.segment(*s, true)) return;
 }
 
 // ------------------------------------------------------------------ products
 // A place in the ring and the parity of its fill.
 struct RingPos {
   uint32_t slot = 0, phase = 0;
-  __device__ void move(uint32_t n) {  // n < kRing
-    slot += n;
-    if (slot >= kRing) slot -= kRing, phase ^= 1u;
-  }
-  __device__ RingPos at(uint32_t n) const {
-    RingPos r = *this;
-    r.move(n);
+  __device__ RingPos next() {  // this one; moves on
+    const RingPos r = *this;
+    if (++slot == kRing) slot = 0, phase ^= 1u;
     return r;
   }
 };
 
+// The products of half t: S(i) and O += P(i) V, one warp a half (see elect_one),
+// so that one's waits and signals pass while the other's products run; each
+// keeps its own order, in which S(i + 2) follows PV(i).  One warp for both took
+// 3500 clocks a unit where its products take 2700.
 struct Issuer {
   uint64_t* bars;
   uint8_t* sR;
-  uint32_t tmem, dq, dk, dv, el, pf;  // descriptors of Q, and of ring slot 0 as K and as V; P's parities, a bit each
+  int t;
+  uint32_t tS, tO, dk, dv, el;  // tensor memory; descriptors of ring slot 0 as K and as V
   const WaitCtl& w;
+  uint32_t s_count = 0, p_count = 0;  // S and P so far: buffer count & 1, parity (count >> 1) & 1
 
   __device__ __forceinline__ bool loaded(const RingPos& r) const { return warp_wait(&bars[B_RF + r.slot], r.phase, w); }
   __device__ __forceinline__ void release(const RingPos& r) const { mma_commit_el(&bars[B_RE + r.slot], el); }
-  // S of half t, keys [64 h, 64 h + 64) of the tile
-  __device__ __forceinline__ void scores(int t, int h, const RingPos& r, uint32_t q) const {
-    mma_tile(tmem + t * 128 + h * 64, q, dk + r.slot * (kTile >> 4) + h * (8192 >> 4), idesc_bf16(128, 64, 0, 0), el);
-    mma_commit_el(&bars[B_SF + 2 * t + h], el);
+  // The next S: queries q, the K in slot r.
+  __device__ __forceinline__ void scores(const RingPos& r, uint32_t q) {
+    const uint32_t buf = s_count++ & 1u;
+    mma_tile<kStepKeys>(tS + buf * 64, q, dk + r.slot * (kSlot >> 4), idesc_bf16(128, kStepKeys, 0, 0), el);
+    mma_commit_el(&bars[B_SF + 2 * t + buf], el);
   }
-  // O += P V over `valid` keys of the same
-  __device__ __forceinline__ bool values(int t, int h, const RingPos& r, int valid, bool first) {
-    if (!warp_wait(&bars[B_PF + 2 * t + h], (pf >> (2 * t + h)) & 1, w)) return false;
-    pf ^= 1u << (2 * t + h);
-    tc_fence_after();
-    const uint32_t id = idesc_bf16(128, 128, 0, 1);
-    const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128 + h * 64, b = dv + r.slot * (kTile >> 4) + h * (8192 >> 4);
-    if (uniform(valid >= 64)) {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
-    } else {
-      for (int kk = 0; uniform(kk * 16 < valid); ++kk) mma_ts_el(o, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
-    }
-    mma_commit_el(&bars[B_PD + t], el);
-    return true;
-  }
-  // Clears a V tile's rows past the stream's keys (up to the product's 16).
-  __device__ __forceinline__ void clear(const RingPos& r, int valid) const {
-    if (uniform(valid < 128 && (valid & 15))) {
-      uint8_t* tile = sR + r.slot * kTile;
+  // O += P V: the next P, the V in slot r, of which `valid` rows count.
+  __device__ __forceinline__ bool values(const RingPos& r, int valid, bool first) {
+    const uint32_t buf = p_count & 1u;
+    if (!warp_wait(&bars[B_PF + 2 * t + buf], (p_count >> 1) & 1u, w)) return false;
+    ++p_count;
+    if (uniform(valid < kStepKeys && (valid & 15))) {  // rows past the stream's keys, up to the product's 16
+      uint8_t* tile = sR + r.slot * kSlot;
       for (int x = valid * 8 + int(threadIdx.x & 31); x < ((valid + 15) & ~15) * 8; x += 32) {
         *reinterpret_cast<uint4*>(tile + x * 16) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(tile + kHalfTile + x * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(tile + kSlot / 2 + x * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_async_smem();
       __syncwarp();
     }
+    tc_fence_after();
+    const uint32_t id = idesc_bf16(128, 128, 0, 1);
+    const uint32_t a = tS + buf * 64, b = dv + r.slot * (kSlot >> 4);
+    if (uniform(valid >= kStepKeys)) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_ts_el(tO, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
+    } else {
+      for (int kk = 0; uniform(kk * 16 < valid); ++kk) mma_ts_el(tO, a + kk * 8, b + kk * 128, id, kk > 0 || !first, el);
+    }
+    mma_commit_el(&bars[B_PD + t], el);
+    return true;
   }
 };
 
-// One warp (see elect_one).
-__device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t* sQ, uint8_t* sR, uint32_t tmem,
+__device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t* sQ, uint8_t* sR, uint32_t tmem, int t,
                                          const WaitCtl& w) {
-  Issuer x{bars, sR, tmem, desc_lo(sQ, 16), desc_lo(sR, 16), desc_lo(sR, kHalfTile), elect_one(), 0, w};
-  const uint32_t q1 = x.dq + (kTile >> 4);
+  Issuer x{bars, sR, t, tmem + t * 128, tmem + 256 + t * 128, desc_lo(sR, 16), desc_lo(sR, kSlot / 2), elect_one(), w};
+  const uint32_t q0 = desc_lo(sQ, 16), q1 = q0 + t * (kTile >> 4);
   RingPos ring;
   uint32_t qf = 0;
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
-    const int n0 = s->n[0], n1 = s->n[1];
-    int left = s->kv - s->j0 * 128;  // keys from the unit's first tile on
-    if (uniform(n0 == 0 && n1 == 0)) continue;
+    const int n = s->n[t], both = s->n[0] + s->n[1];
+    int left = s->kv - s->j0 * kStepKeys;  // keys from the tile on
+    if (uniform(both == 0)) continue;
     if (!warp_wait(&bars[B_QF], qf, w)) return;
     qf ^= 1u;
     if (uniform(s->dual)) {
-      // K(0) V(0) K(1) V(1) ...; n0 <= n1, as the first tile's tokens are the earlier ones
-      if (!x.loaded(ring)) return;
-      bool has0 = uniform(n0 > 0);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (has0) x.scores(0, h, ring, x.dq);
-        x.scores(1, h, ring, q1);
+      // Both halves walk K(0) K(1) V(0) K(2) V(1) ... and release every tile; half
+      // 0 may have fewer steps (its tokens are the earlier ones).
+      const int all = s->n[1];
+#pragma unroll 1
+      for (int i = 0; uniform(i < 2 && i < all); ++i) {
+        const RingPos k = ring.next();
+        if (!x.loaded(k)) return;
+        if (uniform(i < n)) x.scores(k, q1);
+        x.release(k);
       }
-      x.release(ring);
-      for (int u = 0;; ++u, left -= 128) {
-        const RingPos v = ring.at(1), k = ring.at(2);
-        const bool more0 = uniform(u + 1 < n0), more1 = uniform(u + 1 < n1);
-        if (!more1) mma_commit_el(&bars[B_QE], x.el);  // every S of the segment has been issued
+#pragma unroll 2
+      for (int i = 0; uniform(i < all); ++i, left -= kStepKeys) {
+        const RingPos v = ring.next();
         if (!x.loaded(v)) return;
-        x.clear(v, left);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (has0 && !x.values(0, h, v, left - 64 * h, u == 0 && h == 0)) return;
-          if (more1 && h == 0 && !x.loaded(k)) return;
-          if (more0) x.scores(0, h, k, x.dq);
-          if (!x.values(1, h, v, left - 64 * h, u == 0 && h == 0)) return;
-          if (more1) x.scores(1, h, k, q1);
-        }
+        if (uniform(i < n) && !x.values(v, left, i == 0)) return;
         x.release(v);
-        if (has0 && !more0) mma_commit_el(&bars[B_OF], x.el);
-        ring.move(2);
-        if (!more1) break;
-        x.release(ring);
-        has0 = more0;
-      }
-      mma_commit_el(&bars[B_OF + 1], x.el);
-    } else {
-      // tiles y = 2 u + t: K(0) K(1) V(0) K(2) V(1) K(3) ... V(n - 2) V(n - 1)
-      const int n = n0 + n1;
-      const bool two = uniform(n1 > 0);
-      if (!x.loaded(ring)) return;
-      if (two && !x.loaded(ring.at(1))) return;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x.scores(0, h, ring, x.dq);
-        if (two) x.scores(1, h, ring.at(1), x.dq);
-      }
-      x.release(ring);
-      if (two) x.release(ring.at(1));
-      ring.move(two ? 2 : 1);  // now at V(2 u)
-      for (int u = 0;; ++u, left -= 256) {
-        // units in pairs of tiles: V(2 u) [K(2 u + 2)] [V(2 u + 1)] [K(2 u + 3)]
-        const bool has1 = uniform(2 * u + 1 < n), more0 = uniform(2 * u + 2 < n), more1 = uniform(2 * u + 3 < n);
-        const RingPos v0 = ring, k0 = ring.at(1), v1 = ring.at(more0 ? 2 : 1), k1 = ring.at(3);
-        if (!more0) mma_commit_el(&bars[B_QE], x.el);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 0) {
-            if (!x.loaded(v0)) return;
-            x.clear(v0, left);
-          }
-          if (!x.values(0, h, v0, left - 64 * h, u == 0 && h == 0)) return;
-          if (h == 1) x.release(v0);
-          if (more0) {
-            if (h == 0 && !x.loaded(k0)) return;
-            x.scores(0, h, k0, x.dq);
-            if (h == 1) x.release(k0);
-          }
-          if (has1) {
-            if (h == 0) {
-              if (!x.loaded(v1)) return;
-              x.clear(v1, left - 128);
-            }
-            if (!x.values(1, h, v1, left - 128 - 64 * h, u == 0 && h == 0)) return;
-            if (h == 1) x.release(v1);
-          }
-          if (more1) {
-            if (h == 0 && !x.loaded(k1)) return;
-            x.scores(1, h, k1, x.dq);
-            if (h == 1) x.release(k1);
-          }
+        if (uniform(i + 2 < all)) {
+          const RingPos k = ring.next();
+          if (!x.loaded(k)) return;
+          if (uniform(i + 2 < n)) x.scores(k, q1);
+          x.release(k);
         }
-        if (has1 && !more1) mma_commit_el(&bars[B_OF + 1], x.el);
-        ring.move(1 + (more0 ? 1 : 0) + (has1 ? 1 : 0));
-        if (more1) ring.move(1);
-        if (!more0) break;
       }
-      mma_commit_el(&bars[B_OF], x.el);
+    } else {
+      // Tile y is half y & 1's: K(0) .. K(3) V(0) K(4) V(1) K(5) ...  Both halves
+      // wait for and release every tile: who skipped the other's could run a
+      // round of the ring ahead of it, where a parity says nothing.
+#pragma unroll 1
+      for (int y = 0; uniform(y < 4 && y < both); ++y) {
+        const RingPos k = ring.next();
+        if (!x.loaded(k)) return;
+        if (uniform((y & 1) == t)) x.scores(k, q0);
+        x.release(k);
+      }
+#pragma unroll 2
+      for (int y = 0; uniform(y < both); ++y, left -= kStepKeys) {
+        const bool mine = uniform((y & 1) == t);
+        const RingPos v = ring.next();
+        if (!x.loaded(v)) return;
+        if (mine && !x.values(v, left, y < 2)) return;
+        x.release(v);
+        if (uniform(y + 4 < both)) {
+          const RingPos k = ring.next();
+          if (!x.loaded(k)) return;
+          if (mine) x.scores(k, q0);
+          x.release(k);
+        }
+      }
     }
+    mma_commit_el(&bars[B_QE], x.el);
+    if (uniform(n > 0)) mma_commit_el(&bars[B_OF + t], x.el);
   }
 }
 
@@ -422,15 +425,15 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
   const float2 sc = make_float2(p.scale_log2, p.scale_log2);
   uint32_t g = 0, of = 0, merges = 0;  // g: steps so far
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
-    const int rows = s->rows[t], n = 2 * s->n[t], skip = s->dual ? 0 : 128;
+    const int rows = s->rows[t], n = s->n[t], step = s->dual ? kStepKeys : 2 * kStepKeys;
     const bool live = row < rows, warp_live = quarter * 32 < rows;
     int left = s->kv;  // visible keys from the step's first on
     if (live)
       left = visible_keys(SeqView{0, s->n_new, s->kv}, p.mask, s->tok0 + (s->dual ? t * p.qt : 0) + p.per_group.div(row));
-    left -= (s->j0 + (s->dual ? 0 : t)) * 128;
+    left -= (s->j0 + (s->dual ? 0 : t)) * kStepKeys;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i, ++g) {
-      const uint32_t buf = g & 1;  // (a segment has an even number of steps)
+      const uint32_t buf = g & 1;
       if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
       if (warp_live) {
         tc_fence_after();
@@ -488,7 +491,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[B_PF + 2 * t + buf]);
-      left -= 64 + (i & 1 ? skip : 0);
+      left -= step;
     }
     const bool have = n > 0;
     if (have) {
@@ -583,7 +586,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
 }
 
 constexpr int kSmem = 232448;
-constexpr int kLayout = 2 * kTile + kRing * kTile + 256 * 4 + kSegs * int(sizeof(Seg)) + 8 * B_COUNT + 16;
+constexpr int kLayout = 2 * kTile + kRing * kSlot + 256 * 4 + kSegs * int(sizeof(Seg)) + 8 * B_COUNT + 16;
 static_assert(kLayout <= kSmem, "shared memory");
 
 // ------------------------------------------------------------------ kernel
@@ -600,7 +603,7 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   }
   uint8_t* sQ = smem;
   uint8_t* sR = smem + 2 * kTile;
-  float* stats = reinterpret_cast<float*>(sR + kRing * kTile);  // half 1's m, l
+  float* stats = reinterpret_cast<float*>(sR + kRing * kSlot);  // half 1's m, l
   Seg* segs = reinterpret_cast<Seg*>(stats + 256);
   uint64_t* bars = reinterpret_cast<uint64_t*>(segs + kSegs);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B_COUNT);
@@ -608,7 +611,10 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const int n = (i >= B_PF && i < B_PD) || i == B_MG || i == B_MD ? 4 : i >= B_GE && i < B_GE + kSegs ? 10 : 1;
+      const int n = (i >= B_PF && i < B_PD) || i == B_MG || i == B_MD   ? 4
+                    : i >= B_GE && i < B_GE + kSegs                     ? 11
+                    : i == B_QE || (i >= B_RE && i < B_RE + kRing) || i == B_DRAIN ? 2
+                                                                        : 1;
       mbar_init(&bars[i], n);
     }
     *abort_flag = 0;
@@ -629,18 +635,18 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   const WaitCtl w{abort_flag, p.err, p.wait_limit_ns};
   const SegReader reader{segs, bars};
   if (warp == 0) {
-    load_role(p, &tm_q, &tm_k, &tm_v, reader, bars, sQ, sR, w);
-  } else if (warp == 1) {
-    mma_role(reader, bars, sQ, sR, tmem, w);
+    k_role(p, &tm_q, &tm_k, bars, segs, sQ, sR, w);
+  } else if (warp == 1 || warp == 3) {
+    mma_role(reader, bars, sQ, sR, tmem, warp >> 1, w);
   } else if (warp == 2) {
-    seg_role(p, bars, segs, w);
+    v_role(p, &tm_v, reader, bars, sR, w);
   } else if (warp >= 4) {
     softmax_role(p, reader, bars, stats, tmem, (warp >> 2) - 1, w);
   }
   // Every product has completed once a commit behind all of them has arrived:
   // only then are shared and tensor memory released.
   __syncwarp();
-  if (warp == 1) {
+  if (warp == 1 || warp == 3) {
     mma_commit_el(&bars[B_DRAIN], elect_one());
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&bars[B_DRAIN], 0) && global_timer_ns() - t0 < 10000000ull) {

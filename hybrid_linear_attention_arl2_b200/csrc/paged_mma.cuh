@@ -65,13 +65,14 @@ __device__ __forceinline__ void mma_commit_el(uint64_t* bar, uint32_t el) {
       : "memory");
 }
 
-// D = A B^T over K = 128, both K-major tiles of 128 rows.
+// D = A B^T over K = 128, both K-major tiles in two boxes of 64 columns: A of
+// 128 rows, B of kRowsB.
+template <int kRowsB>
 __device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t el) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = (kk >> 2) * (kHalfTile >> 4) + (kk & 3) * 2;
-    mma_ss_el(d, a + off, b + off, idesc, kk > 0, el);
-  }
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ss_el(d, a + (kk >> 2) * (kHalfTile >> 4) + (kk & 3) * 2, b + (kk >> 2) * (kRowsB * 128 >> 4) + (kk & 3) * 2, idesc,
+              kk > 0, el);
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
@@ -101,6 +102,7 @@ __device__ __forceinline__ void store_sector(void* p, const uint32_t (&v)[8]) {
 // after them are on their way while these are used.  A box without a key, or
 // whose table entry is no page, gets the row past the pool's last, which reads
 // as zeros.
+template <int kKeys>  // of a tile
 struct BoxRows {
   const int32_t* table;
   FastDiv page;
@@ -111,7 +113,7 @@ struct BoxRows {
 
   __device__ int key_of(int tile0) const {
     const int lane = threadIdx.x & 31;
-    return lane < per * boxes ? tile0 * 128 + lane * box : 0x7fffffff;
+    return lane < per * boxes ? tile0 * kKeys + lane * box : 0x7fffffff;
   }
   __device__ int fetch(int tile0) const {
     const int k = key_of(tile0);
@@ -130,7 +132,7 @@ struct BoxRows {
   }
   // tiles [tile0, tile1) of stream b
   __device__ BoxRows(const PagedSeqs& s, int b, int kv_, int hk_, int kv_heads_, int tile0, int tile1, uint32_t* err_)
-      : table(s.pages + int64_t(b) * s.pages_ld), page(s.page), box(s.box), boxes(s.boxes), per(s.per), kv(kv_),
+      : table(s.pages + int64_t(b) * s.pages_ld), page(s.page), box(s.box), boxes(kKeys / s.box), per(32 / boxes), kv(kv_),
         n_pages(s.n_pages), hk(hk_), kv_heads(kv_heads_), end(tile1), err(err_) {
     const int pg = fetch(tile0);
     ahead = fetch(tile0 + per);
@@ -147,7 +149,7 @@ struct BoxRows {
     if (i >= 0 && i < boxes) {
       uint8_t* d = dst + i * box * 128;
       tma_load_3d(d, tm, bar, 0, row, 0);
-      tma_load_3d(d + kHalfTile, tm, bar, 64, row, 0);
+      tma_load_3d(d + kKeys * 128, tm, bar, 64, row, 0);
     }
   }
 };

@@ -223,7 +223,7 @@ __device__ __forceinline__ void load_role(const PagedWeightParams& p, const CUte
   bool more = walk.next(p, qt);
   while (more) {  // a (stream, key head) at a time: its key tiles lie in a row
     const int b = walk.u.b, hk = walk.u.hk;
-    BoxRows rows(p.s, b, walk.s.v.kv, hk, p.kv_heads, 2 * walk.u.jt, 2 * walk.s.n_kb, p.err);
+    BoxRows<128> rows(p.s, b, walk.s.v.kv, hk, p.kv_heads, 2 * walk.u.jt, 2 * walk.s.n_kb, p.err);
     for (; more && walk.u.b == b && walk.u.hk == hk; more = walk.next(p, qt)) {
       const Unit& u = walk.u;
       if (u.first) {
@@ -275,7 +275,7 @@ __device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, 
     for (int t = 0; t < 2; ++t) {
       if (g >= 2 && !warp_wait(&bars[B_SC + 2 * t + buf], ((g >> 1) - 1) & 1, w)) return;
       tc_fence_after();
-      mma_tile(tmem + (2 * t + buf) * 128, dk + (2 * i + t) * (kTile >> 4), dq + old * (kTile >> 4), id, el);
+      mma_tile<128>(tmem + (2 * t + buf) * 128, dk + (2 * i + t) * (kTile >> 4), dq + old * (kTile >> 4), id, el);
       mma_commit_el(&bars[B_SF + 2 * t + buf], el);
     }
     if (u.last) mma_commit_el(&bars[B_KE + i], el);

@@ -485,3 +485,18 @@ def test_bounded_stream(dtype, H, hk, d):
         kv = n
         assert kv.tolist() == [min(budget, (rnd + 1) * chunk)] * 2 if rnd < 3 else [budget] * 2
     assert layer.last_error() == 0
+
+
+def test_ragged_calls_back_to_back():
+    """Many launches in a row over short and long streams, single tokens and chunks, give the first one's bits."""
+    seqs = [(1, n) for n in (1, 2, 17, 64, 65, 127, 129, 200, 640, 1000, 2049)] + [(40, 300), (1, 3000), (17, 17), (150, 1200)]
+    c = Paged("bf16", 16, 2, 128, 16, seqs, 77).to_gpu()
+    q = c.randn(c.T, 16, 128).cuda()
+    first = c.layer.attend(c.batch, q, mask_block=1)
+    w = torch.zeros(len(seqs), 2, c.width, device="cuda")
+    w0 = c.layer.weights(c.batch, q, first[1], w, mask_block=1)
+    outs = [(c.layer.attend(c.batch, q, mask_block=1), c.layer.weights(c.batch, q, first[1], w, mask_block=1))
+            for _ in range(200)]
+    ok(c.layer)
+    for (o, lse), x in outs:
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1]) and torch.equal(x, w0)
