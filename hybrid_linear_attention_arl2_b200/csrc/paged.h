@@ -169,8 +169,10 @@ cudaError_t launch_paged_attn_f32(PagedAttnParams p, int grid, cudaStream_t st);
 // bf16 operands travel by TMA: maps over the pools (made once) and the queries
 bool paged_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int page_size);
 bool paged_query_map(CUtensorMap* m, const void* q, int64_t tokens, int heads, int group, int64_t ld);
+// rotate: CTAs take the key tiles of their segments in an order that brings
+// those on one key head together (PagedWalk::rotation)
 cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   cudaStream_t st);
+                                   bool rotate, cudaStream_t st);
 cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st);
 cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensorMap& tk, int sms, cudaStream_t st);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t st);
@@ -281,6 +283,7 @@ template <class Plan>
 struct PagedWalk {
   int each, more;  // cost of every range; the first `more` have one more
   int at, end;     // cost before the current item, and where the range ends
+  int used;        // units of the segments before
   bool have, fresh;
   PagedSeg<Plan> seg;
 
@@ -307,7 +310,7 @@ struct PagedWalk {
     }
     total = __reduce_add_sync(0xffffffffu, mine);
     const int ctas = min(total, grid);
-    at = end = 0;
+    at = end = used = 0;
     have = fresh = true;
     if (cta >= ctas) return;
     each = total / ctas;
@@ -374,8 +377,17 @@ struct PagedWalk {
     }
     return false;
   }
+  // Where to begin within the segment's units, cyclically: the CTAs on one key
+  // head then reach a key tile at about the same time, each at the unit that is
+  // its clock modulo a range's length where its segment has it.
+  __device__ int rotation() const {
+    int r = (used - seg.u0) % each;
+    if (r < 0) r += each;
+    return r < seg.u1 - seg.u0 ? r : 0;
+  }
   // After a segment's use: moves on to the next item where this one ended.
   __device__ void done(const PagedAttnParams& p) {
+    used += seg.u1 - seg.u0;
     if (seg.u1 < seg.blk.units) {
       at = end;
       return;

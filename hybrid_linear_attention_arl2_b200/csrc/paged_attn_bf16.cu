@@ -70,13 +70,14 @@ struct Seg {
   int n_new, kv;       // the stream's new tokens and cached keys
   int dual;            // two tiles of rows on the same key tiles; else one tile on alternate ones
   int n[2];            // steps of 64 keys of each half
+  int rot;             // step with which both halves begin, of their n (cyclic)
   int j0;              // first step's tile of 64 keys (dual: of both; else of half 0, half 1's is the next)
   int rows[2];         // rows of each half's tile
   int slot;            // of this CTA's piece, and the pieces of the item (PagedSeg)
   int owner, pieces, owner_slot;
 };
 
-__device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, const PagedAttnParams& p) {
+__device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, int rotation, const PagedAttnParams& p) {
   const int qt = p.qt;
   g.more = 1;
   g.b = p.per_blk.div(s.f), g.hk = s.hk;
@@ -100,6 +101,7 @@ __device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, const 
     g.n[1] = n >> 1;
     g.rows[0] = g.rows[1] = s.blk.n_tok * p.group;
   }
+  g.rot = g.dual && g.n[0] == g.n[1] ? max(0, min(2 * rotation, g.n[1] - 1)) : 0;
   g.slot = s.slot;
   g.owner = s.owner, g.pieces = s.pieces, g.owner_slot = s.owner_slot;
 }
@@ -148,21 +150,26 @@ struct Loader {
     skip();
     return true;
   }
-  // This warp's tiles of a segment.
+  // This warp's tiles of a segment, from its rotation's on and then those before.
+  template <bool kRotate>
   __device__ __forceinline__ bool segment(const Seg& s, bool is_v) {
-    const int n = s.dual ? s.n[1] : s.n[0] + s.n[1], first = s.dual ? 2 : 4, j0 = s.j0;
-    BoxRows<kStepKeys> rows(p.s, s.b, s.kv, s.hk, p.kv_heads, j0, j0 + n, p.err);
+    const int n = s.dual ? s.n[1] : s.n[0] + s.n[1], first = s.dual ? 2 : 4, j0 = s.j0, rot = kRotate ? s.rot : 0, wrap = n - rot;
+    BoxRows<kStepKeys> rows(p.s, s.b, s.kv, s.hk, p.kv_heads, j0 + rot, j0 + n, p.err);
+    auto take = [&](int i) {
+      if (kRotate && i == wrap) rows = BoxRows<kStepKeys>(p.s, s.b, s.kv, s.hk, p.kv_heads, j0, j0 + rot, p.err);
+      return load(rows, !kRotate || i < wrap ? j0 + rot + i : j0 + i - wrap);
+    };
     for (int i = -first; i < n; ++i) {
       if (i >= 0) {
         if (!is_v)
           skip();
-        else if (!load(rows, j0 + i))
+        else if (!take(i))
           return false;
       }
       if (i + first < n) {
         if (is_v)
           skip();
-        else if (!load(rows, j0 + i + first))
+        else if (!take(i + first))
           return false;
       }
     }
@@ -170,6 +177,7 @@ struct Loader {
   }
 };
 
+template <bool kRotate>
 __device__ __forceinline__ void k_role(const PagedAttnParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                        uint64_t* bars, Seg* ring, uint8_t* sQ, uint8_t* sR, const WaitCtl& w) {
   const int lane = threadIdx.x & 31, qt = p.qt;
@@ -183,7 +191,7 @@ __device__ __forceinline__ void k_role(const PagedAttnParams& p, const CUtensorM
     Seg& s = ring[k % kSegs];
     if (lane == 0) {
       if (more)
-        describe(s, walk.seg, p);
+        describe(s, walk.seg, kRotate ? walk.rotation() : 0, p);
       else
         s.more = 0;
       mbar_arrive(&bars[B_GF + k % kSegs]);
@@ -202,15 +210,16 @@ __device__ __forceinline__ void k_role(const PagedAttnParams& p, const CUtensorM
           tma_load_3d(sQ + t * kTile + h * kHalfTile, tm_q, &bars[B_QF], h * 64, s.hk * p.group, s.row0 + t * qt);
     }
     __syncwarp();
-    if (!loader.segment(s, false)) return;
+    if (!loader.segment<kRotate>(s, false)) return;
   }
 }
 
+template <bool kRotate>
 __device__ __forceinline__ void v_role(const PagedAttnParams& p, const CUtensorMap* tm_v, SegReader segs, uint64_t* bars,
                                        uint8_t* sR, const WaitCtl& w) {
   Loader loader{p, bars, sR, tm_v, w};
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w))
-    if (s->n[0] + s->n[1] > 0 && !loader.segment(*s, true)) return;
+    if (s->n[0] + s->n[1] > 0 && !loader.segment<kRotate>(*s, true)) return;
 }
 
 // ------------------------------------------------------------------ products
@@ -272,6 +281,7 @@ struct Issuer {
   }
 };
 
+template <bool kRotate>
 __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t* sQ, uint8_t* sR, uint32_t tmem, int t,
                                          const WaitCtl& w) {
   Issuer x{bars, sR, t, tmem + t * 128, tmem + 256 + t * 128, desc_lo(sR, 16), desc_lo(sR, kSlot / 2), elect_one(), w};
@@ -280,14 +290,14 @@ __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t
   uint32_t qf = 0;
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
     const int n = s->n[t], both = s->n[0] + s->n[1];
-    int left = s->kv - s->j0 * kStepKeys;  // keys from the tile on
+    int left = s->kv - (s->j0 + (kRotate ? s->rot : 0)) * kStepKeys;  // keys from the tile on
     if (uniform(both == 0)) continue;
     if (!warp_wait(&bars[B_QF], qf, w)) return;
     qf ^= 1u;
     if (uniform(s->dual)) {
       // Both halves walk K(0) K(1) V(0) K(2) V(1) ... and release every tile; half
       // 0 may have fewer steps (its tokens are the earlier ones).
-      const int all = s->n[1];
+      const int all = s->n[1], wrap = kRotate ? all - s->rot : -1;
 #pragma unroll 1
       for (int i = 0; uniform(i < 2 && i < all); ++i) {
         const RingPos k = ring.next();
@@ -297,6 +307,7 @@ __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t
       }
 #pragma unroll 2
       for (int i = 0; uniform(i < all); ++i, left -= kStepKeys) {
+        if (kRotate && i == wrap) left += all * kStepKeys;
         const RingPos v = ring.next();
         if (!x.loaded(v)) return;
         if (uniform(i < n) && !x.values(v, left, i == 0)) return;
@@ -417,6 +428,7 @@ __device__ __forceinline__ void join_own(const PagedAttnParams& p, const Seg& s,
 }
 
 // Warpgroup t: tile t's rows, one a thread, 64 keys a step.
+template <bool kRotate>
 __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader segs, uint64_t* bars, float* stats,
                                              uint32_t tmem, int t, const WaitCtl& w) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
@@ -430,9 +442,11 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
     int left = s->kv;  // visible keys from the step's first on
     if (live)
       left = visible_keys(SeqView{0, s->n_new, s->kv}, p.mask, s->tok0 + (s->dual ? t * p.qt : 0) + p.per_group.div(row));
-    left -= (s->j0 + (s->dual ? 0 : t)) * kStepKeys;
+    left -= (s->j0 + (kRotate ? s->rot : 0) + (s->dual ? 0 : t)) * kStepKeys;
+    const int wrap = kRotate ? n - s->rot : -1;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i, ++g) {
+      if (kRotate && i == wrap) left += n * step;
       const uint32_t buf = g & 1;
       if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
       if (warp_live) {
@@ -590,6 +604,7 @@ constexpr int kLayout = 2 * kTile + kRing * kSlot + 256 * 4 + kSegs * int(sizeof
 static_assert(kLayout <= kSmem, "shared memory");
 
 // ------------------------------------------------------------------ kernel
+template <bool kRotate>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnParams p) {
@@ -635,13 +650,13 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   const WaitCtl w{abort_flag, p.err, p.wait_limit_ns};
   const SegReader reader{segs, bars};
   if (warp == 0) {
-    k_role(p, &tm_q, &tm_k, bars, segs, sQ, sR, w);
+    k_role<kRotate>(p, &tm_q, &tm_k, bars, segs, sQ, sR, w);
   } else if (warp == 1 || warp == 3) {
-    mma_role(reader, bars, sQ, sR, tmem, warp >> 1, w);
+    mma_role<kRotate>(reader, bars, sQ, sR, tmem, warp >> 1, w);
   } else if (warp == 2) {
-    v_role(p, &tm_v, reader, bars, sR, w);
+    v_role<kRotate>(p, &tm_v, reader, bars, sR, w);
   } else if (warp >= 4) {
-    softmax_role(p, reader, bars, stats, tmem, (warp >> 2) - 1, w);
+    softmax_role<kRotate>(p, reader, bars, stats, tmem, (warp >> 2) - 1, w);
   }
   // Every product has completed once a commit behind all of them has arrived:
   // only then are shared and tensor memory released.
@@ -693,13 +708,14 @@ bool paged_query_map(CUtensorMap* m, const void* q, int64_t tokens, int heads, i
 }
 
 cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                                   cudaStream_t st) {
-  static unsigned done = 0;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_bf16_kernel), kSmem, &done);
+                                   bool rotate, cudaStream_t st) {
+  static unsigned done[2] = {0, 0};
+  const auto kernel = rotate ? paged_attn_bf16_kernel<true> : paged_attn_bf16_kernel<false>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, &done[rotate]);
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
-  return launch_overlapped(paged_attn_bf16_kernel, dim3(unsigned(grid)), kThreads, kSmem, st, 0, tq, tk, tv, p);
+  return launch_overlapped(kernel, dim3(unsigned(grid)), kThreads, kSmem, st, 0, tq, tk, tv, p);
 }
 
 }  // namespace arl2

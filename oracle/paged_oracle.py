@@ -44,9 +44,9 @@ def visible(n, kv, m):
     return [min(max(kv - n + (t // m + 1) * m, 0), kv) for t in range(n)]
 
 
-def attend(q, k_pool, v_pool, seqs, tables, mask, scale=None):
+def attend(q, k_pool, v_pool, seqs, tables, mask, scale=None, rows=None):
     """(o, lse, mag): outputs, logarithms of the sums, and sum_j p_j |v_j|, the
-    scale that a bound of the output's error needs."""
+    scale that a bound of the output's error needs.  rows: only these (token rows)."""
     q = np.asarray(q, np.float64)
     T, H, d = q.shape
     hk = k_pool.shape[1]
@@ -55,7 +55,7 @@ def attend(q, k_pool, v_pool, seqs, tables, mask, scale=None):
     for (n, kv), table in zip(seqs, tables):
         K, V = gather(k_pool, table, kv), gather(v_pool, table, kv)
         for t, lim in enumerate(visible(n, kv, mask)):
-            if lim == 0:
+            if lim == 0 or (rows is not None and at + t not in rows):
                 continue
             for h in range(H):
                 g = h // (H // hk)

@@ -500,3 +500,22 @@ def test_ragged_calls_back_to_back():
     ok(c.layer)
     for (o, lse), x in outs:
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1]) and torch.equal(x, w0)
+
+
+@pytest.mark.parametrize("mask", [0, 64])
+def test_chunks_on_a_pool_larger_than_l2(mask):
+    """Several blocks of rows on one key head: CTAs begin inside their key ranges (the pool does not fit L2)."""
+    seqs = [(700, 2500), (300, 300), (1, 500), (513, 1111)]
+    c = Paged("bf16", 4, 2, 128, 64, seqs, 9, spare=2300)
+    c.to_gpu()
+    assert 2 * c.kp.numel() * 2 > torch.cuda.get_device_properties(0).L2_cache_size
+    q = c.randn(c.T, 4, 128).cuda()
+    o, lse = c.layer.attend(c.batch, q, mask_block=mask)
+    ok(c.layer)
+    used = torch.unique(c.tables[c.tables >= 0]).long()
+    kp, vp = np.zeros(c.kp.shape, np.float32), np.zeros(c.vp.shape, np.float32)
+    kp[used], vp[used] = np.nan_to_num(host(c.kp[used])), np.nan_to_num(host(c.vp[used]))
+    rows = np.r_[0:2, 127:130, 255:257, 511:513, 640:645, 699:705, 999:1003, 1250:1270, c.T - 3:c.T]  # of every block's kind
+    ref, ref_l, mag = po.attend(host(q), kp, vp, seqs, c.tables.numpy(), mask, rows=set(rows.tolist()))
+    bo, bl = attend_bounds("bf16", 128, host(q), kp[used].astype(np.float64), c.width, mag, ref)
+    assert (np.abs(host(o) - ref) <= bo)[rows].all() and (np.abs(host(lse) - ref_l) <= bl)[rows].all()
