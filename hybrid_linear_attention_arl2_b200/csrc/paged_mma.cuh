@@ -130,6 +130,7 @@ struct BoxRows {
     }
     first = tile0;
   }
+  __device__ BoxRows() {}
   // tiles [tile0, tile1) of stream b
   __device__ BoxRows(const PagedSeqs& s, int b, int kv_, int hk_, int kv_heads_, int tile0, int tile1, uint32_t* err_)
       : table(s.pages + int64_t(b) * s.pages_ld), page(s.page), box(s.box), boxes(kKeys / s.box), per(32 / boxes), kv(kv_),

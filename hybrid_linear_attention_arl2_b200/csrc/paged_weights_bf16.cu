@@ -16,9 +16,12 @@
 // also clears what lies past kv_len.  Sums run in the order of rows: the same
 // bits every time.
 //
-// Warps: 0 loads, 1 issues the products, 2 puts the rows' lse next to their
-// tile; four warpgroups sum, one for each key tile and half of the columns.  Tensor memory: S^T of tile t,
-// buffer i at columns (2 t + i) 128.
+// Warps: 0 finds the range, describes its blocks and loads K; 2 loads Q and puts
+// the rows' lse next to it; 1 and 3 issue the products, a key tile each; four
+// warpgroups sum, one for each key tile and half of the columns.  What a unit
+// needs beyond its block's description is a few sums: with a walk over streams,
+// heads and blocks in every role a unit took 2000 clocks without any arithmetic.
+// Tensor memory: S^T of tile t, buffer i at columns (2 t + i) 128.
 
 #include "layer.h"
 #include "paged_mma.cuh"
@@ -30,23 +33,25 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kKeys = 256;  // of a block
-constexpr int kQRing = 3;
+constexpr int kQRing = 3, kBlks = 3;
 
 enum {
   B_KF = 0,              // [2] a block's K loaded (bytes)
-  B_KE = 2,              // [2] read (commit)
+  B_KE = 2,              // [2] read (two commits)
   B_QF = 4,              // [kQRing] a Q tile loaded (bytes)
-  B_QE = B_QF + kQRing,  // [kQRing] read (commit)
+  B_QE = B_QF + kQRing,  // [kQRing] read (two commits)
   B_LF = B_QE + kQRing,  // [kQRing] its rows' lse in shared memory (warp 2)
   B_LE = B_LF + kQRing,  // [kQRing] read (16 warps)
   B_SF = B_LE + kQRing,  // [t][2] S^T in tensor memory (commit)
   B_SC = B_SF + 4,       // [t][2] read (8 warps)
   B_JF = B_SC + 4,       // [t] half 1's sums in shared memory (4 warps)
   B_JE = B_JF + 2,       // [t] read (4 warps)
-  B_DRAIN = B_JE + 2,
+  B_GF = B_JE + 2,       // [kBlks] block described
+  B_GE = B_GF + kBlks,   // [kBlks] description read (Q loader, issuers, 16 summing warps)
+  B_DRAIN = B_GE + kBlks,
   B_COUNT
 };
-constexpr int kSmem = 232448, kLayout = 2 * 2 * kTile + kQRing * kTile + kQRing * 512 + 1024 + 8 * B_COUNT + 16;
+constexpr int kSmem = 232448, kLayout = 2 * 2 * kTile + kQRing * kTile + kQRing * 512 + 1024 + kBlks * 56 + 8 * B_COUNT + 16;
 static_assert(kLayout <= kSmem, "shared memory");
 
 // A stream's units.  Row tile rt holds tokens [rt qt, ...); key block jt is
@@ -54,11 +59,15 @@ static_assert(kLayout <= kSmem, "shared memory");
 struct Stream {
   SeqView v;
   int n_kb, n_rt;  // key blocks, row tiles; 0 where nothing is to be summed
+  int full;        // blocks that every row tile sees
   __device__ Stream() {}
-  __device__ Stream(const PagedSeqs& s, int b, int qt, uint32_t* err) : v(load_seq(s, b, err)) {
+  __device__ Stream(const PagedWeightParams& p, int b, uint32_t* err) : v(load_seq(p.s, b, err)) {
     const bool some = v.n > 0 && v.kv > 0;
     n_kb = some ? (v.kv + kKeys - 1) / kKeys : 0;
-    n_rt = some ? (v.n + qt - 1) / qt : 0;
+    n_rt = some ? p.per_tile.div(v.n - 1) + 1 : 0;
+    // blocks that begin below the keys which the first token sees
+    const long long seen = (long long)(v.kv - v.n) + p.mask.by;
+    full = p.mask.by <= 0 ? n_kb : seen <= 0 ? 0 : int(min((long long)n_kb, (seen + kKeys - 1) / kKeys));
   }
   // the first token that sees key j
   __device__ int first_token(const FastDiv& mask, int j) const {
@@ -67,250 +76,241 @@ struct Stream {
     return past < mask.by ? 0 : past - mask.mod(past);
   }
   __device__ int first_tile(const PagedWeightParams& p, int jt) const {
-    return p.per_tile.div(first_token(p.mask, jt * kKeys));
+    return jt < full ? 0 : p.per_tile.div(first_token(p.mask, jt * kKeys));
   }
-  __device__ long long units(const PagedWeightParams& p) const {
-    if (n_kb == 0) return 0;
-    if (p.mask_block <= 0) return (long long)n_kb * n_rt;
-    const long long all = (long long)(v.kv - v.n) + p.mask_block;  // blocks that begin below it are seen by every tile
-    long long full = all <= 0 ? 0 : (all + kKeys - 1) / kKeys;
-    if (full > n_kb) full = n_kb;
-    long long sum = full * n_rt;
-    for (int jt = int(full); jt < n_kb; ++jt) sum += n_rt - first_tile(p, jt);
+  __device__ int units(const PagedWeightParams& p) const {
+    int sum = full * n_rt;
+    for (int jt = full; jt < n_kb; ++jt) sum += n_rt - first_tile(p, jt);
     return sum;
   }
 };
 
-struct Unit {
-  int b, hk, jt, rt;
-  bool first, last;    // of the block's units, within this CTA's range
-  bool starts, ends;   // the range has the block's very first unit; this is its very last
-  bool head;           // of the range's first block
+// A key block as the roles need it: its units [rt0, rt1) within this CTA's range.
+struct Blk {
+  int more, b, hk, jt;
+  int rt0, rt1;
+  int q0, n, kv;
+  int fresh, pad[2];  // its first unit's Q tile is not the last one of the block before
+  int flags, slot;  // 1: holds the block's first unit, 2: its last; slot of its piece
 };
+static_assert(sizeof(Blk) == 56 && kBlks * 56 % 8 == 0, "shared memory");
 
-// The units of a CTA's range in order.
+// The CTA's range, walked block by block, by one warp.
 struct Walk {
   Stream s;
-  Unit u;
-  long long left;
-  bool begun, fresh;
-  __device__ bool next(const PagedWeightParams& p, int qt) {
-    if (left <= 0) return false;
-    if (!begun) {
-      s = Stream(p.s, u.b, qt, nullptr);
-      begun = u.head = true;
-    } else if (++u.rt >= s.n_rt) {
-      if (++u.jt >= s.n_kb) {
-        u.jt = 0;
-        if (++u.hk >= p.kv_heads) {
-          u.hk = 0;
+  int b, hk, jt, rt, left;
+  int qb, qhk, qrt;  // the Q tile before
+  bool head;
+
+  __device__ void find(const PagedWeightParams& p) {
+    const int lane = threadIdx.x & 31;
+    left = 0, qb = -1, qhk = qrt = 0, head = true;
+    int mine = 0;
+#pragma unroll 1
+    for (int i = lane; i < p.s.n_seqs; i += 32)
+      mine += Stream(p, i, blockIdx.x == 0 ? p.err : nullptr).units(p) * p.kv_heads;
+    const int total = __reduce_add_sync(0xffffffffu, mine), ctas = min(total, int(gridDim.x)), cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int each = total / ctas, more = total - each * ctas;
+    int pos = each * cta + min(cta, more);
+    const int len = each + (cta < more ? 1 : 0);
+    // the index in [0, n) whose cost holds `pos`, and pos within it
+    auto find_in = [&](int n, auto&& cost) {
+      int before = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int c = i0 + lane < n ? cost(i0 + lane) : 0;
+        int inc = c;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        const int off = pos - (before + inc - c);
+        const unsigned hit = __ballot_sync(0xffffffffu, off >= 0 && off < c);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          pos = __shfl_sync(0xffffffffu, off, src);
+          return i0 + src;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      return -1;
+    };
+    b = find_in(p.s.n_seqs, [&](int i) { return Stream(p, i, nullptr).units(p) * p.kv_heads; });
+    if (b < 0) return;  // (cannot happen: the range lies inside the units)
+    s = Stream(p, b, nullptr);
+    const int per = s.units(p);
+    hk = pos / per;
+    pos -= hk * per;
+    if (pos < s.full * s.n_rt) {
+      jt = pos / s.n_rt;
+      rt = pos - jt * s.n_rt;
+    } else {
+      pos -= s.full * s.n_rt;
+      jt = s.full + find_in(s.n_kb - s.full, [&](int i) { return s.n_rt - s.first_tile(p, s.full + i); });
+      rt = s.first_tile(p, jt) + pos;
+    }
+    left = len;
+  }
+  // Describes the next block (lane 0 writes) and moves on.
+  __device__ bool next(const PagedWeightParams& p, Blk& out) {
+    const bool writes = (threadIdx.x & 31) == 0;
+    if (left <= 0) {
+      if (writes) out.more = 0;
+      return false;
+    }
+    const int r0 = s.first_tile(p, jt), rt1 = min(s.n_rt, rt + left);
+    if (writes) {
+      out.more = 1;
+      out.b = b, out.hk = hk, out.jt = jt;
+      out.rt0 = rt, out.rt1 = rt1;
+      out.q0 = s.v.q0, out.n = s.v.n, out.kv = s.v.kv;
+      out.fresh = !(qb == b && qhk == hk && qrt == rt);
+      out.flags = (rt == r0 ? 1 : 0) | (rt1 == s.n_rt ? 2 : 0);
+      out.slot = head ? 0 : 1;
+    }
+    head = false;
+    qb = b, qhk = hk, qrt = rt1 - 1;
+    left -= rt1 - rt;
+    if (left > 0) {  // (the block is done)
+      if (++jt >= s.n_kb) {
+        jt = 0;
+        if (++hk >= p.kv_heads) {
+          hk = 0;
           do {
-            if (++u.b >= p.s.n_seqs) return false;  // (cannot happen: the range lies inside the units)
-            s = Stream(p.s, u.b, qt, nullptr);
+            if (++b >= p.s.n_seqs) {  // (cannot happen)
+              left = 0;
+              return true;
+            }
+            s = Stream(p, b, nullptr);
           } while (s.n_kb == 0);
         }
       }
-      u.rt = s.first_tile(p, u.jt);
-      fresh = true;
-      u.head = false;
+      rt = s.first_tile(p, jt);
     }
-    --left;
-    u.first = fresh;
-    if (fresh) u.starts = u.rt == s.first_tile(p, u.jt);
-    fresh = false;
-    u.ends = u.rt == s.n_rt - 1;
-    u.last = u.ends || left == 0;
     return true;
   }
-  __device__ int rows(const PagedWeightParams& p, int qt) const { return min(qt, s.v.n - u.rt * qt) * p.group; }
 };
 
-// Sum of c over threads below this one (its own not counted), and the total.
-__device__ __forceinline__ long long scan(long long c, long long* sh, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long inc = c;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+// The blocks as a role meets them (a whole warp).
+struct BlkReader {
+  const Blk* ring;
+  uint64_t* bars;
+  uint32_t k = 0;
+  __device__ const Blk* next(const WaitCtl& w) {
+    if (!warp_wait(&bars[B_GF + k % kBlks], (k / kBlks) & 1, w)) return nullptr;
+    const Blk* g = &ring[k % kBlks];
+    return g->more ? g : nullptr;
   }
-  __syncthreads();
-  if (lane == 31) sh[warp] = inc;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += sh[i];
-    total += sh[i];
+  __device__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars[B_GE + k % kBlks]);
+    ++k;
   }
-  return before + inc - c;
-}
-
-// Where the CTA's range begins.  sh: 32 shared words.
-__device__ __forceinline__ Walk find_range(const PagedWeightParams& p, int qt, long long* sh) {
-  const int tid = threadIdx.x;
-  Walk w;
-  w.left = 0, w.begun = false, w.fresh = true;
-  auto cost = [&](int b, uint32_t* err) {
-    return b < p.s.n_seqs ? Stream(p.s, b, qt, err).units(p) * p.kv_heads : 0;
-  };
-  long long first = cost(tid, p.err), mine = first, total;
-  for (int b = tid + kThreads; b < p.s.n_seqs; b += kThreads) mine += cost(b, p.err);
-  scan(mine, sh, total);
-  const int ctas = total < gridDim.x ? int(total) : int(gridDim.x), cta = blockIdx.x;
-  if (cta >= ctas) return w;
-  const long long u0 = total * cta / ctas;
-  w.left = total * (cta + 1) / ctas - u0;
-  long long base = 0;
-  for (int b0 = 0; b0 < p.s.n_seqs; b0 += kThreads) {
-    const long long c = b0 == 0 ? first : cost(b0 + tid, nullptr);
-    long long all;
-    const long long beg = base + scan(c, sh, all);
-    if (c > 0 && u0 >= beg && u0 < beg + c) {
-      sh[24] = b0 + tid;
-      sh[25] = u0 - beg;
-    }
-    __syncthreads();
-    base += all;
-    if (u0 < base) break;
-  }
-  w.u.b = int(sh[24]);
-  const Stream s(p.s, w.u.b, qt, nullptr);
-  const long long per = s.units(p);
-  w.u.hk = int(sh[25] / per);
-  const long long off = sh[25] % per;
-  // the key block: a second search over the stream's blocks
-  base = 0;
-  for (int j0 = 0; j0 < s.n_kb; j0 += kThreads) {
-    const int jt = j0 + tid, r0 = jt < s.n_kb ? s.first_tile(p, jt) : 0;
-    const long long c = jt < s.n_kb ? s.n_rt - r0 : 0;
-    long long all;
-    const long long beg = base + scan(c, sh, all);
-    if (c > 0 && off >= beg && off < beg + c) {
-      sh[26] = jt;
-      sh[27] = r0 + (off - beg);
-    }
-    __syncthreads();
-    base += all;
-    if (off < base) break;
-  }
-  w.u.jt = int(sh[26]);
-  w.u.rt = int(sh[27]);
-  __syncthreads();
-  return w;
-}
-
-// Which slot of the Q ring a unit reads: units of neighbouring blocks that
-// read the same tile (single tokens) share a slot.
-struct QSlot {
-  int b = -1, hk = 0, rt = 0;
-  uint32_t count = 0;  // tiles so far; the current one is count - 1
-  __device__ bool step(const Unit& u) {  // true: a new tile
-    if (u.b == b && u.hk == hk && u.rt == rt) return false;
-    b = u.b, hk = u.hk, rt = u.rt;
-    ++count;
-    return true;
-  }
-  __device__ uint32_t slot() const { return (count - 1) % kQRing; }
-  __device__ uint32_t parity() const { return ((count - 1) / kQRing) & 1; }
 };
 
-__device__ __forceinline__ void load_role(const PagedWeightParams& p, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                                          Walk walk, int qt, uint64_t* bars, uint8_t* sK, uint8_t* sQ,
-                                          const WaitCtl& w) {
+// A place in the Q ring.
+struct QPos {
+  uint32_t slot = kQRing - 1, round = 0xffffffffu;  // before the first
+  __device__ void next() {
+    if (++slot == kQRing) slot = 0, ++round;
+  }
+};
+
+__device__ __forceinline__ void k_role(const PagedWeightParams& p, const CUtensorMap* tm_k, uint64_t* bars, Blk* ring,
+                                       uint8_t* sK, const WaitCtl& w) {
   const int lane = threadIdx.x & 31;
-  QSlot q;
-  uint32_t blocks = 0;
-  bool more = walk.next(p, qt);
-  while (more) {  // a (stream, key head) at a time: its key tiles lie in a row
-    const int b = walk.u.b, hk = walk.u.hk;
-    BoxRows<128> rows(p.s, b, walk.s.v.kv, hk, p.kv_heads, 2 * walk.u.jt, 2 * walk.s.n_kb, p.err);
-    for (; more && walk.u.b == b && walk.u.hk == hk; more = walk.next(p, qt)) {
-      const Unit& u = walk.u;
-      if (u.first) {
-        const uint32_t i = blocks & 1;
-        if (blocks >= 2 && !warp_wait(&bars[B_KE + i], ((blocks >> 1) - 1) & 1, w)) return;
-        if (lane == 0) mbar_expect_tx(&bars[B_KF + i], 2 * kTile);
-        __syncwarp();
+  Walk walk;
+  walk.find(p);
+  int b = -1, hk = -1;
+  BoxRows<128> rows;
+  for (uint32_t k = 0;; ++k) {
+    if (k >= kBlks && !warp_wait(&bars[B_GE + k % kBlks], (k / kBlks - 1) & 1, w)) return;
+    Blk& blk = ring[k % kBlks];
+    const bool more = walk.next(p, blk);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[B_GF + k % kBlks]);
+    if (!more) return;
+    if (blk.b != b || blk.hk != hk) {  // a (stream, key head): its key tiles lie in a row
+      b = blk.b, hk = blk.hk;
+      rows = BoxRows<128>(p.s, b, blk.kv, hk, p.kv_heads, 2 * blk.jt, 2 * ((blk.kv + kKeys - 1) / kKeys), p.err);
+    }
+    const uint32_t i = k & 1;
+    if (k >= 2 && !warp_wait(&bars[B_KE + i], ((k >> 1) - 1) & 1, w)) return;
+    if (lane == 0) mbar_expect_tx(&bars[B_KF + i], 2 * kTile);
+    __syncwarp();
 #pragma unroll
-        for (int t = 0; t < 2; ++t) rows.load(2 * u.jt + t, sK + (2 * i + t) * kTile, tm_k, &bars[B_KF + i]);
-        __syncwarp();
-        ++blocks;
+    for (int t = 0; t < 2; ++t) rows.load(2 * blk.jt + t, sK + (2 * i + t) * kTile, tm_k, &bars[B_KF + i]);
+    __syncwarp();
+  }
+}
+
+// Q tiles, and their rows' -lse log2(e): -inf where a row adds nothing.
+__device__ __forceinline__ void q_role(const PagedWeightParams& p, const CUtensorMap* tm_q, BlkReader blks, int qt,
+                                       uint64_t* bars, uint8_t* sQ, float* sL, const WaitCtl& w) {
+  const int lane = threadIdx.x & 31;
+  QPos q;
+  for (const Blk* k = blks.next(w); k; blks.done(), k = blks.next(w)) {
+    for (int rt = k->fresh ? k->rt0 : k->rt0 + 1; rt < k->rt1; ++rt) {
+      q.next();
+      const int tok = rt * qt, rows = min(qt, k->n - tok) * p.group;
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = lane + 32 * i, t = p.per_group.div(r);
+        x[i] = -INFINITY;
+        if (r < rows) x[i] = p.lse[int64_t(k->q0 + tok + t) * p.heads + k->hk * p.group + (r - t * p.group)];
       }
-      if (q.step(u)) {
-        if (q.count > kQRing && !warp_wait(&bars[B_QE + q.slot()], q.parity() ^ 1, w)) return;
-        if (lane == 0) {
-          mbar_expect_tx(&bars[B_QF + q.slot()], 2u * uint32_t(qt * p.group) * 128u);
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(sQ + q.slot() * kTile + h * kHalfTile, tm_q, &bars[B_QF + q.slot()], h * 64, hk * p.group,
-                        walk.s.v.q0 + u.rt * qt);
-        }
-        __syncwarp();
+      if (q.round > 0 && !warp_wait(&bars[B_QE + q.slot], (q.round - 1) & 1, w)) return;
+      if (lane == 0) {
+        mbar_expect_tx(&bars[B_QF + q.slot], 2u * uint32_t(qt * p.group) * 128u);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(sQ + q.slot * kTile + h * kHalfTile, tm_q, &bars[B_QF + q.slot], h * 64, k->hk * p.group, k->q0 + tok);
       }
+      if (q.round > 0 && !warp_wait(&bars[B_LE + q.slot], (q.round - 1) & 1, w)) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sL[q.slot * 128 + lane + 32 * i] = x[i] == -INFINITY ? x[i] : -1.4426950408889634f * x[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_LF + q.slot]);
     }
   }
 }
 
-// One warp (see elect_one).
-__device__ __forceinline__ void mma_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, uint8_t* sK,
-                                         uint8_t* sQ, uint32_t tmem, const WaitCtl& w) {
-  const uint32_t dk = desc_lo(sK, 16), dq = desc_lo(sQ, 16);
-  const uint32_t el = elect_one();
-  QSlot q;
-  uint32_t blocks = 0, g = 0, old = 0;
-  while (walk.next(p, qt)) {
-    const Unit& u = walk.u;
-    if (u.first) {
-      if (!warp_wait(&bars[B_KF + (blocks & 1)], (blocks >> 1) & 1, w)) return;
-      ++blocks;
-    }
-    const uint32_t i = (blocks - 1) & 1;
-    if (q.step(u)) {
-      if (q.count > 1) mma_commit_el(&bars[B_QE + old], el);
-      old = q.slot();
-      if (!warp_wait(&bars[B_QF + old], q.parity(), w)) return;
-    }
-    const int rows = walk.rows(p, qt);
-    const uint32_t id = idesc_bf16(128, (rows + 15) & ~15, 0, 0), buf = g & 1;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
+// The products of key tile t (one warp, see elect_one).
+__device__ __forceinline__ void mma_role(const PagedWeightParams& p, BlkReader blks, int qt, uint64_t* bars, uint8_t* sK,
+                                         uint8_t* sQ, uint32_t tmem, int t, const WaitCtl& w) {
+  const uint32_t dk = desc_lo(sK + t * kTile, 16), dq = desc_lo(sQ, 16), el = elect_one();
+  QPos q;
+  uint32_t g = 0;
+  for (const Blk* k = blks.next(w); k; blks.done(), k = blks.next(w)) {
+    const uint32_t i = blks.k & 1;
+    if (!warp_wait(&bars[B_KF + i], (blks.k >> 1) & 1, w)) return;
+    const int rt0 = k->rt0, units = k->rt1 - rt0, fresh = k->fresh;
+    int tokens = k->n - rt0 * qt;  // from the unit's first on
+#pragma unroll 2
+    for (int u = 0; uniform(u < units); ++u, tokens -= qt) {
+      if (uniform(u > 0 || fresh)) {
+        if (uniform(q.round != 0xffffffffu)) mma_commit_el(&bars[B_QE + q.slot], el);
+        q.next();
+        if (!warp_wait(&bars[B_QF + q.slot], q.round & 1, w)) return;
+      }
+      const uint32_t buf = g & 1;
       if (g >= 2 && !warp_wait(&bars[B_SC + 2 * t + buf], ((g >> 1) - 1) & 1, w)) return;
       tc_fence_after();
-      mma_tile<128>(tmem + (2 * t + buf) * 128, dk + (2 * i + t) * (kTile >> 4), dq + old * (kTile >> 4), id, el);
+      const uint32_t cols = (min(tokens, qt) * p.group + 15) & ~15;
+      mma_tile<128>(tmem + (2 * t + buf) * 128, dk + 2 * i * (kTile >> 4), dq + q.slot * (kTile >> 4),
+                    idesc_bf16(128, 0, 0, 0) | (cols >> 3) << 17, el);
       mma_commit_el(&bars[B_SF + 2 * t + buf], el);
+      ++g;
     }
-    if (u.last) mma_commit_el(&bars[B_KE + i], el);
-    ++g;
-  }
-}
-
-// Rows' -lse log2(e), a tile ahead of their use; -inf where a row adds nothing.
-__device__ __forceinline__ void lse_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, float* sL,
-                                         const WaitCtl& w) {
-  const int lane = threadIdx.x & 31;
-  QSlot q;
-  while (walk.next(p, qt)) {
-    const Unit& u = walk.u;
-    if (!q.step(u)) continue;
-    const int rows = walk.rows(p, qt);
-    float x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = lane + 32 * i, t = p.per_group.div(r);
-      x[i] = -INFINITY;
-      if (r < rows)
-        x[i] = p.lse[int64_t(walk.s.v.q0 + u.rt * qt + t) * p.heads + u.hk * p.group + (r - t * p.group)];
-    }
-    if (q.count > kQRing && !warp_wait(&bars[B_LE + q.slot()], q.parity() ^ 1, w)) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sL[q.slot() * 128 + lane + 32 * i] = x[i] == -INFINITY ? x[i] : -1.4426950408889634f * x[i];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[B_LF + q.slot()]);
+    mma_commit_el(&bars[B_KE + i], el);
   }
 }
 
 // Pairs of 16 whose exponentials run on the FMA pipe.
-constexpr int kPolyPairs = 5;
+constexpr int kPolyPairs = 3;
 
 // Sum of 2^(s scale + nl) over 32 columns [c0, c0 + 32); with kMask only those
 // in [lo, hi).
@@ -339,78 +339,80 @@ __device__ __forceinline__ float2 sum_chunk(const uint32_t* r, const float4* nl,
 
 // Warpgroup (t, half): key tile t, columns [64 half, 64 half + 64) of each unit.
 // Half 1 hands its sums of a block to half 0 through sJ.
-__device__ __forceinline__ void sum_role(const PagedWeightParams& p, Walk walk, int qt, uint64_t* bars, const float* sL,
+__device__ __forceinline__ void sum_role(const PagedWeightParams& p, BlkReader blks, int qt, uint64_t* bars, const float* sL,
                                          float* sJ, uint32_t tmem, int t, int half, const WaitCtl& w) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
   const uint32_t tS = tmem + t * 256 + half * 64 + (uint32_t(quarter * 32) << 16);
   const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-  QSlot q;
-  uint32_t g = 0, old = 0, blocks = 0;
-  float sum = 0.f;
-  while (walk.next(p, qt)) {
-    const Unit& u = walk.u;
-    if (q.step(u)) {
-      if (q.count > 1) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_LE + old]);
-      }
-      old = q.slot();
-      if (!warp_wait(&bars[B_LF + old], q.parity(), w)) return;
-    }
-    const int key = u.jt * kKeys + t * 128 + row, rows = walk.rows(p, qt);
+  const int col0 = half * 64;
+  QPos q;
+  uint32_t g = 0;
+  for (const Blk* k = blks.next(w); k; blks.done(), k = blks.next(w)) {
+    const int key = k->jt * kKeys + t * 128 + row, units = k->rt1 - k->rt0;
     // the key is seen by the tile's columns [lo, rows)
-    const long long from = (long long)(walk.s.first_token(p.mask, key) - u.rt * qt) * p.group;
-    const int lo = from < 0 ? 0 : from > 128 ? 128 : int(from);
-    const bool masked = __any_sync(0xffffffffu, lo > 0) || rows < 128;
-    const uint32_t buf = g & 1;
-    if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
-    ++g;
-    tc_fence_after();
-    const float4* nl = reinterpret_cast<const float4*>(sL + old * 128 + half * 64);
-    float2 acc = make_float2(0.f, 0.f);
-    // (columns from the product's width on hold an older product, and are masked)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t r[32];
-      const bool some = half * 64 + 32 * c < rows;
-      if (some) {
-        tmem_ld32(tS + buf * 128 + c * 32, r);
-        tmem_wait_ld();
-      }
-      if (c == 1) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_SC + 2 * t + buf]);
-      }
-      if (!masked)
-        acc = sum_chunk<false>(r, nl + 8 * c, sc, 0, 0, 0, acc);
-      else if (some)
-        acc = sum_chunk<true>(r, nl + 8 * c, sc, half * 64 + 32 * c, lo, rows, acc);
+    int from = 0;  // tokens from the unit's first on that do not see it
+    if (p.mask.by > 0) {
+      Stream s;
+      s.v = SeqView{0, k->n, k->kv};
+      from = s.first_token(p.mask, key) - k->rt0 * qt;
     }
-    sum += acc.x + acc.y;
-    if (u.last) {
-      if (half == 1) {
-        if (blocks > 0 && !warp_wait(&bars[B_JE + t], (blocks - 1) & 1, w)) return;
-        sJ[t * 128 + row] = sum;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_JF + t]);
-      } else {
-        if (!warp_wait(&bars[B_JF + t], blocks & 1, w)) return;
-        sum += sJ[t * 128 + row];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_JE + t]);
-        const bool whole = u.starts && u.ends;
-        const int piece = 2 * blockIdx.x + (u.head ? 0 : 1);
-        if (whole) {
-          const int64_t at = (int64_t(u.b) * p.kv_heads + u.hk) * p.w_ld + key;
-          if (key < walk.s.v.kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], sum);
-        } else {
-          p.part_w[piece * kKeys + t * 128 + row] = sum;
-          if (t == 0 && row == 0) p.rec[piece] = make_int4(u.b, u.hk, u.jt, (u.starts ? 1 : 0) | (u.ends ? 2 : 0));
+    int tokens = k->n - k->rt0 * qt;
+    float2 sum = make_float2(0.f, 0.f);
+    for (int u = 0; u < units; ++u, tokens -= qt, from -= qt) {
+      if (u > 0 || k->fresh) {
+        if (q.round != 0xffffffffu) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_LE + q.slot]);
         }
+        q.next();
+        if (!warp_wait(&bars[B_LF + q.slot], q.round & 1, w)) return;
       }
-      ++blocks;
-      sum = 0.f;
+      const uint32_t buf = g & 1;
+      if (!warp_wait(&bars[B_SF + 2 * t + buf], (g >> 1) & 1, w)) return;
+      ++g;
+      tc_fence_after();
+      const int rows = min(tokens, qt) * p.group, lo = from <= 0 ? 0 : min(from, qt) * p.group;
+      const bool masked = rows < 128 || __any_sync(0xffffffffu, lo > 0);
+      const float4* nl = reinterpret_cast<const float4*>(sL + q.slot * 128 + col0);
+      // (columns from the product's width on hold an older product, and are masked)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        const bool some = col0 + 32 * c < rows;
+        if (some) {
+          tmem_ld32(tS + buf * 128 + c * 32, r);
+          tmem_wait_ld();
+        }
+        if (c == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_SC + 2 * t + buf]);
+        }
+        if (!masked)
+          sum = sum_chunk<false>(r, nl + 8 * c, sc, 0, 0, 0, sum);
+        else if (some)
+          sum = sum_chunk<true>(r, nl + 8 * c, sc, col0 + 32 * c, lo, rows, sum);
+      }
+    }
+    float total = sum.x + sum.y;
+    if (half == 1) {
+      if (blks.k > 0 && !warp_wait(&bars[B_JE + t], (blks.k - 1) & 1, w)) return;
+      sJ[t * 128 + row] = total;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_JF + t]);
+    } else {
+      if (!warp_wait(&bars[B_JF + t], blks.k & 1, w)) return;
+      total += sJ[t * 128 + row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_JE + t]);
+      if (k->flags == 3) {
+        const int64_t at = (int64_t(k->b) * p.kv_heads + k->hk) * p.w_ld + key;
+        if (key < k->kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], total);
+      } else {
+        const int piece = 2 * blockIdx.x + k->slot;
+        p.part_w[piece * kKeys + t * 128 + row] = total;
+        if (t == 0 && row == 0) p.rec[piece] = make_int4(k->b, k->hk, k->jt, k->flags);
+      }
     }
   }
 }
@@ -431,13 +433,19 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   uint8_t* sQ = smem + 4 * kTile;    // [kQRing]
   float* sL = reinterpret_cast<float*>(sQ + kQRing * kTile);  // [kQRing][128]
   float* sJ = sL + kQRing * 128;  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sJ + 256);
+  Blk* blks = reinterpret_cast<Blk*>(sJ + 256);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(blks) + kBlks * sizeof(Blk));
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, qt = 128 / p.group;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(&bars[i], i >= B_LE && i < B_LE + kQRing ? 16 : i >= B_SC && i < B_JF ? 8 : i >= B_JF && i < B_DRAIN ? 4 : 1);
+      mbar_init(&bars[i], i == B_KE || i == B_KE + 1 || (i >= B_QE && i < B_QE + kQRing) || i == B_DRAIN ? 2
+                          : i >= B_LE && i < B_LE + kQRing                                             ? 16
+                          : i >= B_SC && i < B_JF                                                      ? 8
+                          : i >= B_JF && i < B_GF                                                      ? 4
+                          : i >= B_GE && i < B_DRAIN                                                   ? 19
+                                                                                                       : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -449,25 +457,25 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   grid_dependency_wait();
   allow_dependent_launch();
   if (threadIdx.x < 2) p.rec[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
-  const Walk walk = find_range(p, qt, reinterpret_cast<long long*>(sL));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const WaitCtl w{abort_flag, p.err, p.wait_limit_ns};
+  const BlkReader reader{blks, bars};
   if (warp == 0) {
-    load_role(p, &tm_q, &tm_k, walk, qt, bars, sK, sQ, w);
-  } else if (warp == 1) {
-    mma_role(p, walk, qt, bars, sK, sQ, tmem, w);
+    k_role(p, &tm_k, bars, blks, sK, w);
   } else if (warp == 2) {
-    lse_role(p, walk, qt, bars, sL, w);
-  } else if (warp >= 4) {
+    q_role(p, &tm_q, reader, qt, bars, sQ, sL, w);
+  } else if (warp < 4) {
+    mma_role(p, reader, qt, bars, sK, sQ, tmem, warp >> 1, w);
+  } else {
     const int wg = (warp >> 2) - 1;
-    sum_role(p, walk, qt, bars, sL, sJ, tmem, wg & 1, wg >> 1, w);
+    sum_role(p, reader, qt, bars, sL, sJ, tmem, wg & 1, wg >> 1, w);
   }
   // shared and tensor memory are released once a commit behind every product has arrived
   __syncwarp();
-  if (warp == 1) {
+  if (warp == 1 || warp == 3) {
     mma_commit_el(&bars[B_DRAIN], elect_one());
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&bars[B_DRAIN], 0) && global_timer_ns() - t0 < 10000000ull) {
