@@ -91,7 +91,7 @@ struct PagedWeightParams {
   FastDiv mask, per_group, per_tile;  // by mask_block, group, a tile's tokens
   float scale_log2;
   float* part_w;        // bf16: [2 * grid][256] sums of key blocks that CTAs share
-  int4* rec;            // [2 * grid] (stream, key head, key block, starts | ends << 1) of those pieces
+  uint32_t* joined;     // as PagedAttnParams'
   uint32_t* err;
   uint64_t wait_limit_ns;
 };

@@ -112,9 +112,8 @@ struct arl2_paged {
   float scale;
   void *k_pool, *v_pool;
   uint64_t wait_ns;
-  float* part_o;   // pieces of items that CTAs share, their statistics and records (PagedAttnParams)
+  float* part_o;   // pieces of items that CTAs share, and their statistics (PagedAttnParams)
   float2* part_ml;
-  int4* rec;        // (weights)
   uint32_t* joined;
   int grid;        // CTAs of the attention launch
   uint32_t* err;
@@ -135,7 +134,7 @@ bool live(const arl2_paged* h) {
 }
 
 void free_paged(arl2_paged* h) {
-  for (void* p : {(void*)h->part_o, (void*)h->part_ml, (void*)h->rec, (void*)h->joined, (void*)h->err})
+  for (void* p : {(void*)h->part_o, (void*)h->part_ml, (void*)h->joined, (void*)h->err})
     if (p) cudaFree(p);
   h->magic = 0;
   delete h;
@@ -309,10 +308,8 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
   h->grid = paged_attn_grid(cfg->dtype, h->sms);
   const size_t pieces = 2 * size_t(h->grid), rows = paged_piece_rows(cfg->dtype);
   const size_t po = pieces * rows * cfg->head_dim * sizeof(float), pm = pieces * rows * sizeof(float2);
-  const size_t pr = pieces * sizeof(int4);
   cudaError_t e = device_alloc(reinterpret_cast<void**>(&h->part_o), po);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->part_ml), pm);
-  if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->rec), pr);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->joined), joined_bytes(h));
   if (e == cudaSuccess) e = cudaMemsetAsync(h->joined, 0, joined_bytes(h), h->last_stream);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->err), 256);
@@ -321,7 +318,7 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
     free_paged(h);
     return status_of_cuda(e);
   }
-  h->bytes = int64_t(po + pm + pr + joined_bytes(h) + 256);
+  h->bytes = int64_t(po + pm + joined_bytes(h) + 256);
   h->magic = kPagedMagic;
   {
     std::lock_guard<std::mutex> g(g_paged_mu);
@@ -502,7 +499,7 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
   if (double(batch->n_seqs) * c.kv_heads * (batch->max_kv / 256 + 1) * (batch->max_q / (128 / p.group) + 1) >= 2147483647.0)
     return ARL2_ERR_UNSUPPORTED;
   p.part_w = h->part_o;
-  p.rec = h->rec;
+  p.joined = h->joined;
   PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_weights_bf16(p, h->tm_k, h->sms, h->last_stream)
                                  : launch_paged_weights_f32(p, h->last_stream));
   return ARL2_OK;

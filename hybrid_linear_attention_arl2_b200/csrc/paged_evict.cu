@@ -28,43 +28,47 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ int2 warp_scan(int2 v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) v.x += x, v.y += y;
+  }
+  return v;
+}
 // Sum over the block's threads below this one, and the whole sum.
 __device__ __forceinline__ int2 block_scan(int2 v, int2* sh, int2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int2 inc = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
-    if (lane >= o) inc.x += x, inc.y += y;
-  }
+  const int2 inc = warp_scan(v);
   if (lane == 31) sh[warp] = inc;
   __syncthreads();
-  int2 base = make_int2(0, 0);
-  total = make_int2(0, 0);
-  for (int w = 0; w < kWarps; ++w) {
-    const int2 s = sh[w];
-    if (w < warp) base.x += s.x, base.y += s.y;
-    total.x += s.x, total.y += s.y;
-  }
+  const int2 mine = sh[lane], sums = warp_scan(mine);  // (32 warps, a lane each)
+  static_assert(kWarps == 32, "a lane a warp");
+  total = make_int2(__shfl_sync(0xffffffffu, sums.x, 31), __shfl_sync(0xffffffffu, sums.y, 31));
+  const int bx = __shfl_sync(0xffffffffu, sums.x - mine.x, warp), by = __shfl_sync(0xffffffffu, sums.y - mine.y, warp);
   __syncthreads();
-  return make_int2(base.x + inc.x - v.x, base.y + inc.y - v.y);
+  return make_int2(bx + inc.x - v.x, by + inc.y - v.y);
 }
 
 constexpr int kHeld = 4;                      // keys a thread keeps in registers
 constexpr int kChunk = kThreads * kHeld;      // keys of a round
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ int remote_int(const int* p, uint32_t rank) {
-  int v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_u32(p), rank)) : "memory");
+// Two words of another CTA's shared memory (no barrier is passed on the way, so
+// that the loads of several CTAs' are in flight together).
+__device__ __forceinline__ int2 remote_int2(const int* p, uint32_t rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_map(smem_u32(p), rank)));
   return v;
 }
 
 // One cluster per (stream, key head).
 __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvictParams p, int cluster) {
-  __shared__ int hist[3][kBins];
+  __shared__ __align__(8) int hist[3][kBins];
   __shared__ int2 sh[kWarps];
   __shared__ int found[2];
-  __shared__ int counts[2];
+  __shared__ __align__(8) int counts[2];
   const int item = blockIdx.x / cluster, rank = blockIdx.x - item * cluster, tid = threadIdx.x;
   const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
   grid_dependency_wait();
@@ -120,9 +124,12 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvict
       // the digit in which the need-th largest lies: bins from the top, two a thread
       const int b0 = kBins - 1 - 2 * tid;
       int c0 = 0, c1 = 0;
-      for (int q = 0; q < cluster; ++q) {
-        c0 += remote_int(&h[b0], q);
-        c1 += remote_int(&h[b0 - 1], q);
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q < cluster) {
+          const int2 c = remote_int2(&h[b0 - 1], q);
+          c0 += c.y, c1 += c.x;
+        }
       }
       int2 total;
       const int above = block_scan(make_int2(c0 + c1, 0), sh, total).x;
@@ -154,9 +161,12 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvict
   if (tid < 2) counts[tid] = tid == 0 ? total.x : total.y;
   cluster_barrier();
   int2 before = make_int2(0, 0);
-  for (int q = 0; q < rank; ++q) {
-    before.x += remote_int(&counts[0], q);
-    before.y += remote_int(&counts[1], q);
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) {
+    if (q < rank) {
+      const int2 c = remote_int2(counts, q);
+      before.x += c.x, before.y += c.y;
+    }
   }
   for (int r = 0; r < rounds; ++r) {
     int2 mine = make_int2(0, 0);

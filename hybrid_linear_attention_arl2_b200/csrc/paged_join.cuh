@@ -34,11 +34,11 @@ __device__ __forceinline__ int64_t piece_at(int64_t first, int row, int col8) {
 }
 
 // Rows [r0, r0 + n) of a piece's kPieceRows, n <= 32, by one warp: the lanes
-// hold the rows' statistics; then eight rows at a time, a lane's four columns
-// each.  `out(r)`: row r's index in O's [token, head] rows.  kLanes: the piece
+// hold the rows' statistics; then kRows rows at a time, a lane's four columns
+// each, kUnroll pieces in flight.  `out(r)`: row r's index in O's [token, head] rows.  kLanes: the piece
 // is laid out for a thread a row (piece_at), else row by row.
-template <typename T, int kPieceRows, bool kLanes, class Out>
-__device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
+template <typename T, int kPieceRows, bool kLanes, int kRows, int kUnroll, class Out>
+__device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
                                           const Out& out) {
   const int lane = threadIdx.x & 31, d = p.d;
   auto piece = [&](int k) { return int64_t(k == 0 ? 2 * owner + owner_slot : 2 * (owner + k)) * kPieceRows + r0; };
@@ -49,19 +49,19 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, i
   }
   if (M == -INFINITY) M = 0.f;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    float4 acc[8];
+  for (int i0 = 0; i0 < n; i0 += kRows) {
+    float4 acc[kRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     L = 0.f;
-#pragma unroll 2
+#pragma unroll kUnroll
     for (int k = 0; k < pieces; ++k) {
       const int64_t at = piece(k);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < n) ml = __ldcg(&p.part_ml[at + lane]);
-      float4 v[8];
+      float4 v[kRows];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + i < n && lane * 4 < d)
           v[i] = __ldcg(reinterpret_cast<const float4*>(
@@ -70,7 +70,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, i
       const float mine = exp2f(ml.x - M);
       L = fmaf(ml.y, mine, L);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const float w = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
         acc[i] = make_float4(fmaf(v[i].x, w, acc[i].x), fmaf(v[i].y, w, acc[i].y), fmaf(v[i].z, w, acc[i].z),
                              fmaf(v[i].w, w, acc[i].w));
@@ -78,7 +78,7 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, i
     }
     const float rcp = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       const float inv = __shfl_sync(0xffffffffu, rcp, (i0 + i) & 31);
       if (i0 + i < n && lane * 4 < d)
         store4(static_cast<T*>(p.o) + out(r0 + i0 + i) * d + lane * 4,
@@ -86,6 +86,16 @@ __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, i
     }
   }
   if (lane < n && p.lse) p.lse[out(r0 + lane)] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The same, with more pieces in flight where the rows are few.
+template <typename T, int kPieceRows, bool kLanes, class Out>
+__device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
+                                          const Out& out) {
+  if (n <= 2)
+    join_some<T, kPieceRows, kLanes, 2, 8>(p, owner, owner_slot, pieces, r0, n, out);
+  else
+    join_some<T, kPieceRows, kLanes, 8, 2>(p, owner, owner_slot, pieces, r0, n, out);
 }
 
 }  // namespace arl2

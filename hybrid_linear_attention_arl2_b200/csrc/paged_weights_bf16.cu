@@ -12,9 +12,9 @@
 //
 // Work: units (key block, tile of rows that sees it), stream by stream, key head
 // by key head, blocks in order; CTAs take equal contiguous ranges.  A block cut
-// by a range's end is joined from the CTAs' pieces by the finish kernel, which
-// also clears what lies past kv_len.  Sums run in the order of rows: the same
-// bits every time.
+// by a range's end is joined from the CTAs' pieces, in order, by the one that
+// comes last.  Sums run in the order of rows: the same bits every time.  What
+// lies past kv_len is cleared by the summing warps while the range is found.
 //
 // Warps: 0 finds the range, describes its blocks and loads K; 2 loads Q and puts
 // the rows' lse next to it; 1 and 3 issue the products, a key tile each; four
@@ -24,6 +24,7 @@
 // Tensor memory: S^T of tile t, buffer i at columns (2 t + i) 128.
 
 #include "layer.h"
+#include "paged_join.cuh"
 #include "paged_mma.cuh"
 #include "params.h"
 
@@ -90,8 +91,8 @@ struct Blk {
   int more, b, hk, jt;
   int rt0, rt1;
   int q0, n, kv;
-  int fresh, pad[2];  // its first unit's Q tile is not the last one of the block before
-  int flags, slot;  // 1: holds the block's first unit, 2: its last; slot of its piece
+  int fresh;   // its first unit's Q tile is not the last one of the block before
+  int pieces, owner, owner_slot, slot;  // as PagedSeg's
 };
 static_assert(sizeof(Blk) == 56 && kBlks * 56 % 8 == 0, "shared memory");
 
@@ -100,7 +101,14 @@ struct Walk {
   Stream s;
   int b, hk, jt, rt, left;
   int qb, qhk, qrt;  // the Q tile before
+  int each, more, at;  // units of every range (the first `more` have one more); the next unit
   bool head;
+
+  __device__ int begin(int cta) const { return each * cta + min(cta, more); }
+  __device__ int owner(int unit) const {
+    const int big = (each + 1) * more;
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+  }
 
   __device__ void find(const PagedWeightParams& p) {
     const int lane = threadIdx.x & 31;
@@ -111,8 +119,8 @@ struct Walk {
       mine += Stream(p, i, blockIdx.x == 0 ? p.err : nullptr).units(p) * p.kv_heads;
     const int total = __reduce_add_sync(0xffffffffu, mine), ctas = min(total, int(gridDim.x)), cta = blockIdx.x;
     if (cta >= ctas) return;
-    const int each = total / ctas, more = total - each * ctas;
-    int pos = each * cta + min(cta, more);
+    each = total / ctas, more = total - each * ctas;
+    int pos = at = begin(cta);
     const int len = each + (cta < more ? 1 : 0);
     // the index in [0, n) whose cost holds `pos`, and pos within it
     auto find_in = [&](int n, auto&& cost) {
@@ -167,12 +175,19 @@ struct Walk {
       out.rt0 = rt, out.rt1 = rt1;
       out.q0 = s.v.q0, out.n = s.v.n, out.kv = s.v.kv;
       out.fresh = !(qb == b && qhk == hk && qrt == rt);
-      out.flags = (rt == r0 ? 1 : 0) | (rt1 == s.n_rt ? 2 : 0);
       out.slot = head ? 0 : 1;
+      out.pieces = 1, out.owner = out.owner_slot = 0;
+      if (rt > r0 || rt1 < s.n_rt) {
+        const int first = at - (rt - r0);
+        out.owner = owner(first);
+        out.pieces = owner(first + (s.n_rt - r0) - 1) - out.owner + 1;
+        out.owner_slot = begin(out.owner) == first ? 0 : 1;
+      }
     }
     head = false;
     qb = b, qhk = hk, qrt = rt1 - 1;
     left -= rt1 - rt;
+    at += rt1 - rt;
     if (left > 0) {  // (the block is done)
       if (++jt >= s.n_kb) {
         jt = 0;
@@ -405,14 +420,40 @@ __device__ __forceinline__ void sum_role(const PagedWeightParams& p, BlkReader b
       total += sJ[t * 128 + row];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[B_JE + t]);
-      if (k->flags == 3) {
-        const int64_t at = (int64_t(k->b) * p.kv_heads + k->hk) * p.w_ld + key;
-        if (key < k->kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], total);
-      } else {
-        const int piece = 2 * blockIdx.x + k->slot;
-        p.part_w[piece * kKeys + t * 128 + row] = total;
-        if (t == 0 && row == 0) p.rec[piece] = make_int4(k->b, k->hk, k->jt, k->flags);
+      if (k->pieces > 1) {
+        const int mine = t * 128 + row;
+        p.part_w[(2 * blockIdx.x + k->slot) * kKeys + mine] = total;
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = last_piece(p.joined + 8 * k->owner + 4 * t + quarter, k->pieces);
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        total = __ldcg(&p.part_w[(2 * k->owner + k->owner_slot) * kKeys + mine]);
+#pragma unroll 4
+        for (int i = 1; i < k->pieces; ++i) total += __ldcg(&p.part_w[2 * (k->owner + i) * kKeys + mine]);
       }
+      const int64_t at = (int64_t(k->b) * p.kv_heads + k->hk) * p.w_ld + key;
+      if (key < k->kv) p.w_out[at] = fmaf(p.decay, p.w_in[at], total);
+    }
+  }
+}
+
+// What no new token adds to: rows past kv_len are cleared, and the weights of
+// streams without new tokens fade.  Runs of kTail weights, a warp each: `warp` of
+// `warps`.
+constexpr int kTail = 1024;
+__device__ __forceinline__ void clear_tails(const PagedWeightParams& p, int warp, int warps) {
+  const long long per_row = (p.w_ld + kTail - 1) / kTail, items = per_row * p.s.n_seqs * p.kv_heads;
+  for (long long it = warp; it < items; it += warps) {
+    const long long row = it / per_row, j0 = (it - row * per_row) * kTail, j1 = min((long long)p.w_ld, j0 + kTail);
+    const SeqView v = load_seq(p.s, int(row / p.kv_heads), nullptr);
+    if (v.n < 0 || (j1 <= v.kv && v.n > 0)) continue;
+    const int64_t base = row * p.w_ld;
+    for (long long j = j0 + (threadIdx.x & 31); j < j1; j += 32) {
+      if (j >= v.kv)
+        p.w_out[base + j] = 0.f;
+      else if (v.n == 0)
+        p.w_out[base + j] = p.decay * p.w_in[base + j];
     }
   }
 }
@@ -456,7 +497,6 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   }
   grid_dependency_wait();
   allow_dependent_launch();
-  if (threadIdx.x < 2) p.rec[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -470,6 +510,7 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   } else if (warp < 4) {
     mma_role(p, reader, qt, bars, sK, sQ, tmem, warp >> 1, w);
   } else {
+    clear_tails(p, blockIdx.x * 16 + warp - 4, gridDim.x * 16);
     const int wg = (warp >> 2) - 1;
     sum_role(p, reader, qt, bars, sL, sJ, tmem, wg & 1, wg >> 1, w);
   }
@@ -495,50 +536,11 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
   }
 }
 
-// The first `ctas` blocks join the pieces of a key block that CTA ranges cut
-// (that of the CTA which holds its first unit, and slots 0 of the CTAs after it
-// up to the one that ends it); the others clear the rows past kv_len, and fade
-// the weights of streams without new tokens.
-constexpr int kTail = 4096;
-__global__ void __launch_bounds__(kKeys) paged_weights_finish_kernel(const PagedWeightParams p, int ctas) {
+// Where no stream has new tokens.
+__global__ void __launch_bounds__(256) paged_weights_fade_kernel(const PagedWeightParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int tid = threadIdx.x;
-  if (int(blockIdx.x) < ctas) {
-    const int c = blockIdx.x;
-    int slot = -1;
-    int4 rec = p.rec[2 * c];
-    if (rec.x >= 0 && rec.w == 1) slot = 0;
-    if (slot < 0) {
-      rec = p.rec[2 * c + 1];
-      if (rec.x >= 0 && rec.w == 1) slot = 1;
-    }
-    if (slot < 0) return;
-    float sum = p.part_w[(2 * c + slot) * kKeys + tid];
-    for (int i = c + 1; i < ctas; ++i) {
-      sum += p.part_w[2 * i * kKeys + tid];
-      if (p.rec[2 * i].w & 2) break;
-    }
-    const int key = rec.z * kKeys + tid;
-    const int64_t at = (int64_t(rec.x) * p.kv_heads + rec.y) * p.w_ld + key;
-    if (key < p.s.kv_len[rec.x]) p.w_out[at] = fmaf(p.decay, p.w_in[at], sum);
-    return;
-  }
-  const long long per_row = (p.w_ld + kTail - 1) / kTail, items = per_row * p.s.n_seqs * p.kv_heads;
-  for (long long it = blockIdx.x - ctas; it < items; it += gridDim.x - ctas) {
-    const long long row = it / per_row, j0 = it % per_row * kTail;
-    const SeqView v = load_seq(p.s, int(row / p.kv_heads), nullptr);
-    if (v.n < 0) continue;
-    const long long j1 = min((long long)p.w_ld, j0 + kTail);
-    if (j1 <= v.kv && v.n > 0) continue;
-    for (long long j = j0 + tid; j < j1; j += kKeys) {
-      const int64_t at = row * p.w_ld + j;
-      if (j >= v.kv)
-        p.w_out[at] = 0.f;
-      else if (v.n == 0)
-        p.w_out[at] = p.decay * p.w_in[at];
-    }
-  }
+  clear_tails(p, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
 }
 
 }  // namespace
@@ -547,17 +549,11 @@ cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensor
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_bf16_kernel), kSmem, &done);
   if (e != cudaSuccess) return e;
-  int ctas = 0;
-  if (p.s.tokens > 0 && p.s.max_q > 0 && p.s.max_kv > 0) {
-    CUtensorMap tq;
-    if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
-    ctas = sms;
-    e = launch_overlapped(paged_weights_bf16_kernel, dim3(unsigned(ctas)), kThreads, kSmem, st, 0, tq, tk, p);
-    if (e != cudaSuccess) return e;
-  }
-  const long long items = (p.w_ld + kTail - 1) / kTail * p.s.n_seqs * p.kv_heads;
-  return launch_overlapped(paged_weights_finish_kernel, dim3(unsigned(ctas + (items < 65536 ? items : 65536))), kKeys, 0, st,
-                           0, p, ctas);
+  if (p.s.tokens < 1 || p.s.max_q < 1 || p.s.max_kv < 1)
+    return launch_overlapped(paged_weights_fade_kernel, dim3(unsigned(sms)), 256, 0, st, 0, p);
+  CUtensorMap tq;
+  if (!paged_query_map(&tq, p.q, p.s.tokens, p.heads, p.group, p.ld_q)) return cudaErrorInvalidValue;
+  return launch_overlapped(paged_weights_bf16_kernel, dim3(unsigned(sms)), kThreads, kSmem, st, 0, tq, tk, p);
 }
 
 }  // namespace arl2
