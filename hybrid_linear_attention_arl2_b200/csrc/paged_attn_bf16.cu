@@ -305,7 +305,7 @@ __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t
         if (uniform(i < n)) x.scores(k, q1);
         x.release(k);
       }
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; uniform(i < all); ++i, left -= kStepKeys) {
         if (kRotate && i == wrap) left += all * kStepKeys;
         const RingPos v = ring.next();
@@ -330,7 +330,7 @@ __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t
         if (uniform((y & 1) == t)) x.scores(k, q0);
         x.release(k);
       }
-#pragma unroll 2
+#pragma unroll 1
       for (int y = 0; uniform(y < both); ++y, left -= kStepKeys) {
         const bool mine = uniform((y & 1) == t);
         const RingPos v = ring.next();
@@ -351,17 +351,15 @@ __device__ __forceinline__ void mma_role(SegReader segs, uint64_t* bars, uint8_t
 }
 
 // ------------------------------------------------------------------ softmax and output
-// Of the 16 pairs of a 32-column chunk this many take the FMA-pipe exponential.
-constexpr int kPolyPerChunk = 3;
-
-template <bool kPoly>
+// P = 2^(S scale - m) for 32 columns of a row, packed to bf16 pairs; their sum.
+// All on the MUFU: with 3 of 16 pairs on the FMA pipe (a polynomial of degree 4)
+// a frame took 412 us instead of 393, as the products bound the loop.
 __device__ __forceinline__ float exp_chunk(const uint32_t* r, const float2 sc, const float2 nm, uint32_t (&pk)[16]) {
   float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int x = 0; x < 16; ++x) {
     const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])), sc, nm);
-    const bool poly = kPoly && (x % 3 == 1) && (x / 3) < kPolyPerChunk;
-    const float2 e = poly ? exp2_fma_pair(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
+    const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
     s2[x & 1] = __fadd2_rn(s2[x & 1], e);
     pk[x] = pack_bf16x2(e.x, e.y);
   }
@@ -495,7 +493,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t pc[16];
-          sum += masked ? exp_chunk<false>(&r[32 * q], sc, nm, pc) : exp_chunk<true>(&r[32 * q], sc, nm, pc);
+          sum += exp_chunk(&r[32 * q], sc, nm, pc);
           tmem_st16(tS + buf * 64 + q * 16, pc);
         }
         l = fmaf(l, f, sum);

@@ -1,6 +1,6 @@
 // What the paged cache's bf16 kernels share: single-CTA tensor-core
 // instructions with a tensor-memory operand, tiles of keys gathered from pages
-// by TMA, exponentials, and full-sector stores.
+// by TMA, and full-sector stores.
 #pragma once
 
 #include <cuda.h>
@@ -154,43 +154,5 @@ struct BoxRows {
     }
   }
 };
-
-// 2^x for a pair on the FMA pipe: x = n + f, n = round(x) in the low mantissa
-// bits after adding 1.5 * 2^23, 2^f by the polynomial of degree 4 through the
-// five Chebyshev nodes of [-1/2, 1/2] (gen_exp2_poly.py 4; relative error below
-// 3.6e-6), 2^n added to the exponent field.  x is clamped below at -125.
-__device__ __forceinline__ float2 exp2_fma_pair(float2 x) {
-  constexpr float kRound = 12582912.f;
-  constexpr float c0 = 1.f, c1 = 0.693121016f, c2 = 0.240223497f, c3 = 0.0559219755f, c4 = 0.00966636837f;
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
-  const float2 t = __fadd2_rn(x, make_float2(kRound, kRound));
-  const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(kRound, kRound), make_float2(-t.x, -t.y)));
-  float2 q = __ffma2_rn(make_float2(c4, c4), f, make_float2(c3, c3));
-  q = __ffma2_rn(q, f, make_float2(c2, c2));
-  q = __ffma2_rn(q, f, make_float2(c1, c1));
-  q = __ffma2_rn(q, f, make_float2(c0, c0));
-  return make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + __float_as_uint(q.x)),
-                     __uint_as_float((__float_as_uint(t.y) << 23) + __float_as_uint(q.y)));
-}
-
-// The same with the polynomial of degree 5 (gen_exp2_poly.py 5; relative error
-// below 1.1e-7): where the sum is kept in float32.
-__device__ __forceinline__ float2 exp2_fma_pair5(float2 x) {
-  constexpr float kRound = 12582912.f;
-  constexpr float c0 = 1.00000012f, c1 = 0.693147182f, c2 = 0.240221068f, c3 = 0.0555035695f, c4 = 0.00967603177f,
-                  c5 = 0.00133908633f;
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
-  const float2 t = __fadd2_rn(x, make_float2(kRound, kRound));
-  const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(kRound, kRound), make_float2(-t.x, -t.y)));
-  float2 q = __ffma2_rn(make_float2(c5, c5), f, make_float2(c4, c4));
-  q = __ffma2_rn(q, f, make_float2(c3, c3));
-  q = __ffma2_rn(q, f, make_float2(c2, c2));
-  q = __ffma2_rn(q, f, make_float2(c1, c1));
-  q = __ffma2_rn(q, f, make_float2(c0, c0));
-  return make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + __float_as_uint(q.x)),
-                     __uint_as_float((__float_as_uint(t.y) << 23) + __float_as_uint(q.y)));
-}
 
 }  // namespace arl2

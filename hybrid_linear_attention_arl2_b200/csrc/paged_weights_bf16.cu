@@ -8,7 +8,8 @@
 // stream's rows past them in tiles of 128 (token, head of the group): each tile
 // of Q serves both products, 32 bytes a clock from L2 instead of 64.  Bound: the
 // exponentials (2048 clocks of the MUFU a 256 x 128 unit against the products'
-// 1024), of which a part goes to the FMA pipe; for single tokens the bytes of K.
+// 1024; a part of them on the FMA pipe changed nothing); for single tokens the
+// bytes of K.
 //
 // Work: units (key block, tile of rows that sees it), stream by stream, key head
 // by key head, blocks in order; CTAs take equal contiguous ranges.  A block cut
@@ -324,9 +325,6 @@ __device__ __forceinline__ void mma_role(const PagedWeightParams& p, BlkReader b
   }
 }
 
-// Pairs of 16 whose exponentials run on the FMA pipe.
-constexpr int kPolyPairs = 3;
-
 // Sum of 2^(s scale + nl) over 32 columns [c0, c0 + 32); with kMask only those
 // in [lo, hi).
 template <bool kMask>
@@ -339,8 +337,7 @@ __device__ __forceinline__ float2 sum_chunk(const uint32_t* r, const float4* nl,
     for (int y = 0; y < 2; ++y) {
       float2 e = __ffma2_rn(make_float2(__uint_as_float(r[2 * (x + y)]), __uint_as_float(r[2 * (x + y) + 1])), sc,
                             y == 0 ? make_float2(n4.x, n4.y) : make_float2(n4.z, n4.w));
-      const bool poly = !kMask && (x + y) % 3 == 1 && (x + y) / 3 < kPolyPairs;
-      e = poly ? exp2_fma_pair5(e) : make_float2(fast_exp2(e.x), fast_exp2(e.y));
+      e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
       if (kMask) {
         const int c = c0 + 2 * (x + y);
         e.x = c >= lo && c < hi ? e.x : 0.f;

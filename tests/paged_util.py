@@ -72,14 +72,13 @@ def attend_bounds(dtype, d, q, k, kv, mag, o):
     d steps of float32 of M from its products' sum (a step 2^-24; 2^-22 where the
     tensor core adds without rounding), and by 2^-24 of itself from its scaling
     and its subtraction (it is at most M); an exponential is then off by that
-    much relative, by 2^-21 for its own evaluation, or by 2^-15 where bf16 inputs
-    allow a polynomial; the sums add 2^-24 a key.  A row's output is off by
+    much relative, and by 2^-21 for its own evaluation; the sums add 2^-24 a key.  A row's output is off by
     that relative to sum p |v|, twice (numerator and denominator); bf16 rounds
     the weights and the output, half a step (2^-8) each.
     """
     M = float(np.sqrt((q ** 2).sum(-1).max() * (k ** 2).sum(-1).max())) * d ** -0.5
     add = 2.0 ** (-24 if dtype == "f32" else -22)
-    rel = d * add * M + 4 * 2.0 ** -24 * M + 2.0 ** (-21 if dtype == "f32" else -15) + kv * add + 16 * 2.0 ** -24
+    rel = d * add * M + 4 * 2.0 ** -24 * M + 2.0 ** -21 + kv * add + 16 * 2.0 ** -24
     lse = rel + 2.0 ** -22 * (M + np.log(max(kv, 2)))
     if dtype == "f32":
         return 2 * rel * mag + 2.0 ** -24 * np.abs(o) + 1e-30, lse
