@@ -19,9 +19,9 @@
 // PV(i) S(i + 2);  the loader's ring of 16 KB tiles follows it.  S(i + 2)
 // overwrites P(i) behind PV(i) in the pipe.
 //
-// Warps: 0 loads (Q by one box a tile, K and V by boxes inside pages, one lane a
-// box, page numbers fetched ahead), 1 and 3 issue the products, 2 describes the
-// segments, 4-7 and 8-11 softmax, O's rescaling (only when a row's maximum grows
+// Warps: 0 describes the segments and loads Q (one box a tile) and K, 2 loads V
+// (boxes inside pages, one lane a box, page numbers fetched ahead), 1 and 3 issue
+// the products of a half each, 4-7 and 8-11 softmax, O's rescaling (only when a row's maximum grows
 // by more than 8 in log2 units: P <= 256) and the output; a thread has one row.
 // Tensor memory: S_t, P_t of step i at t 128 + (i & 1) 64; O_t at 256 + t 128.
 //

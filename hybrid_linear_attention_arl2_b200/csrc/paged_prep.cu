@@ -222,7 +222,7 @@ cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cu
   int lpr = 1;
   while (lpr < chunks) lpr *= 2;
   // Parts, a power of two up to a block's groups, until an SM has 256 threads:
-  // a single token's rows go to all of a block's groups, 27000 tokens take one.
+  // a single token's rows go to all of a block's groups, 25000 tokens take one.
   const int groups = kThreads / lpr;
   int parts = 1;
   while (parts < groups && p.tokens * parts * lpr < int64_t(sms) * 256) parts *= 2;
