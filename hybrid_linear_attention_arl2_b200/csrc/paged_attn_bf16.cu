@@ -57,7 +57,8 @@ enum {
   B_RE = B_RF + kRing,   // [kRing] ring slot read (two commits)
   B_GF = B_RE + kRing,   // [kSegs] segment described
   B_GE = B_GF + kSegs,   // [kSegs] description read (the V loader, both issuers, 8 softmax warps)
-  B_DRAIN = B_GE + kSegs,
+  B_JN = B_GE + kSegs,   // [kSegs] the pieces of half 0's warps are in, Seg::last says whether as the last (4 warps)
+  B_DRAIN = B_JN + kSegs,
   B_COUNT
 };
 
@@ -75,11 +76,13 @@ struct Seg {
   int rows[2];         // rows of each half's tile
   int slot;            // of this CTA's piece, and the pieces of the item (PagedSeg)
   int owner, pieces, owner_slot;
+  int last;            // half 0 joins the pieces (said by one of its warps)
 };
 
 __device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, int rotation, const PagedAttnParams& p) {
   const int qt = p.qt;
   g.more = 1;
+  g.last = 0;
   g.b = p.per_blk.div(s.f), g.hk = s.hk;
   g.row0 = s.blk.row0;
   g.tok0 = s.blk.t0;
@@ -433,7 +436,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
   const uint32_t lane_off = uint32_t(quarter * 32) << 16;
   const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * 128 + lane_off;
   const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-  uint32_t g = 0, of = 0, merges = 0;  // g: steps so far
+  uint32_t g = 0, of = 0, merges = 0, asked = 0;  // g: steps so far; asked: parity of each B_JN
   for (const Seg* s = segs.next(w); s; segs.done(), s = segs.next(w)) {
     const int rows = s->rows[t], n = s->n[t], step = s->dual ? kStepKeys : 2 * kStepKeys;
     const bool live = row < rows, warp_live = quarter * 32 < rows;
@@ -544,6 +547,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
     const int64_t piece = int64_t(2 * blockIdx.x + s->slot) * 256;
     const int64_t prow = piece + t * 128 + row;
     const bool sectors = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+    const bool team = !whole && !s->dual;
     if (warp_live) {
       // 32 columns at a time in a loop of its own: code that runs once costs its fetch
 #pragma unroll 1
@@ -574,20 +578,34 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
         else if (p.lse)
           p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
-      if (!whole) {  // the warp whose piece of these rows comes last joins them
+      if (!whole) {
+        // The warp whose piece of these rows comes last joins them, in a dual segment;
+        // else the last of all the rows' warps tells its warpgroup.
         __threadfence();
         __syncwarp();
         int last = 0;
-        if (lane == 0) last = last_piece(p.joined + 8 * s->owner + 4 * t + quarter, s->pieces);
-        if (__shfl_sync(0xffffffffu, last, 0)) {
-          const int n = min(32, rows - quarter * 32);
-          if (n <= 8)  // few rows, and often many pieces: the warp goes through them together
-            join_rows<__nv_bfloat16, 256, true>(p, s->owner, s->owner_slot, s->pieces, t * 128 + quarter * 32, n,
-                                                [&](int r) { return out_row(r - t * 128); });
-          else if (live)
-            join_own(p, *s, t * 128 + row, orow, sectors);
+        if (lane == 0)
+          last = last_piece(p.joined + 8 * s->owner + (team ? 0 : 4 * t + quarter), s->pieces * (team ? (rows + 31) >> 5 : 1));
+        if (team) {
+          if (last) const_cast<Seg*>(s)->last = 1;
+        } else if (__shfl_sync(0xffffffffu, last, 0) && live) {
+          join_own(p, *s, t * 128 + row, orow, sectors);
         }
       }
+    }
+    if (team) {
+      // Often few rows and many pieces: the four warps share the rows.  (A barrier
+      // for each place of the ring of segments: one that all segments shared could
+      // be two phases ahead of a warp.)
+      const uint32_t at = segs.k % kSegs;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_JN + at]);
+      if (!warp_wait(&bars[B_JN + at], (asked >> at) & 1, w)) return;
+      asked ^= 1u << at;
+      const int n = (rows + 3) >> 2;
+      if (uniform(*const_cast<const volatile int*>(&s->last) != 0 && quarter * n < rows))
+        join_rows<__nv_bfloat16, 256, true>(p, s->owner, s->owner_slot, s->pieces, quarter * n, min(n, rows - quarter * n),
+                                            out_row);
     }
     if (join) {  // O_1 and its statistics are read
       tc_fence_before();
@@ -624,7 +642,7 @@ paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const int n = (i >= B_PF && i < B_PD) || i == B_MG || i == B_MD   ? 4
+      const int n = (i >= B_PF && i < B_PD) || i == B_MG || i == B_MD || (i >= B_JN && i < B_JN + kSegs) ? 4
                     : i >= B_GE && i < B_GE + kSegs                     ? 11
                     : i == B_QE || (i >= B_RE && i < B_RE + kRing) || i == B_DRAIN ? 2
                                                                         : 1;

@@ -214,8 +214,9 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
       if (tid == 0) join = last_piece(p.joined + 8 * s.owner, s.pieces);
       __syncthreads();
       if (join) {
-        const int r0 = (tid >> 5) * (kRows / (kThreads / 32));
-        join_rows<float, kRows, false>(p, s.owner, s.owner_slot, s.pieces, r0, min(rows - r0, kRows / (kThreads / 32)), out_row);
+        constexpr int kWarps = kThreads / 32;
+        const int n = (rows + kWarps - 1) / kWarps, r0 = (tid >> 5) * n;
+        join_rows<float, kRows, false>(p, s.owner, s.owner_slot, s.pieces, r0, min(rows - r0, n), out_row);
       }
     }
     __syncthreads();  // sQ is read no more, nor the segment

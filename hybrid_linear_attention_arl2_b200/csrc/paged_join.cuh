@@ -43,7 +43,19 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
   const int lane = threadIdx.x & 31, d = p.d;
   auto piece = [&](int k) { return int64_t(k == 0 ? 2 * owner + owner_slot : 2 * (owner + k)) * kPieceRows + r0; };
   float M = -INFINITY, L = 0.f;
-  if (lane < n) {
+  if (kRows == 2) {  // the lanes share the pieces, 32 at a time
+    float mine[2] = {-INFINITY, -INFINITY};
+    for (int k = lane; k < pieces; k += 32) {
+      mine[0] = fmaxf(mine[0], __ldcg(&p.part_ml[piece(k)].x));
+      if (n > 1) mine[1] = fmaxf(mine[1], __ldcg(&p.part_ml[piece(k) + 1].x));
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+      mine[0] = fmaxf(mine[0], __shfl_xor_sync(0xffffffffu, mine[0], x));
+      mine[1] = fmaxf(mine[1], __shfl_xor_sync(0xffffffffu, mine[1], x));
+    }
+    M = lane == 0 ? mine[0] : lane == 1 ? mine[1] : -INFINITY;
+  } else if (lane < n) {
 #pragma unroll 4
     for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(&p.part_ml[piece(k) + lane].x));
   }
@@ -54,26 +66,33 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
 #pragma unroll
     for (int i = 0; i < kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     L = 0.f;
-#pragma unroll kUnroll
-    for (int k = 0; k < pieces; ++k) {
-      const int64_t at = piece(k);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = __ldcg(&p.part_ml[at + lane]);
-      float4 v[kRows];
+#pragma unroll 1
+    for (int k0 = 0; k0 < pieces; k0 += kUnroll) {
+      float2 ml[kUnroll];
+      float4 v[kUnroll][kRows];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + i < n && lane * 4 < d)
-          v[i] = __ldcg(reinterpret_cast<const float4*>(
-              p.part_o + (kLanes ? piece_at(at - r0, r0 + i0 + i, lane >> 1) + (lane & 1) * 4 : (at + i0 + i) * d + lane * 4)));
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t at = piece(k0 + u);
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (lane < n && k0 + u < pieces) ml[u] = __ldcg(&p.part_ml[at + lane]);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + i < n && lane * 4 < d && k0 + u < pieces)
+            v[u][i] = __ldcg(reinterpret_cast<const float4*>(
+                p.part_o + (kLanes ? piece_at(at - r0, r0 + i0 + i, lane >> 1) + (lane & 1) * 4 : (at + i0 + i) * d + lane * 4)));
+        }
       }
-      const float mine = exp2f(ml.x - M);
-      L = fmaf(ml.y, mine, L);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float w = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
-        acc[i] = make_float4(fmaf(v[i].x, w, acc[i].x), fmaf(v[i].y, w, acc[i].y), fmaf(v[i].z, w, acc[i].z),
-                             fmaf(v[i].w, w, acc[i].w));
+      for (int u = 0; u < kUnroll; ++u) {
+        const float mine = exp2f(ml[u].x - M);
+        L = fmaf(ml[u].y, mine, L);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const float w = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
+          acc[i] = make_float4(fmaf(v[u][i].x, w, acc[i].x), fmaf(v[u][i].y, w, acc[i].y), fmaf(v[u][i].z, w, acc[i].z),
+                               fmaf(v[u][i].w, w, acc[i].w));
+        }
       }
     }
     const float rcp = L > 0.f ? 1.f / L : 0.f;
@@ -88,7 +107,9 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
   if (lane < n && p.lse) p.lse[out(r0 + lane)] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The same, with more pieces in flight where the rows are few.
+// The same, with more pieces in flight where the rows are few: one token of 16
+// heads on 20000 keys (74 pieces a key head) took 90 us when one warp joined
+// all rows, four pieces' statistics and two pieces' rows at a time; 28 us so.
 template <typename T, int kPieceRows, bool kLanes, class Out>
 __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
                                           const Out& out) {

@@ -207,6 +207,27 @@ def test_attend_and_weights(dtype, H, hk, d, page, mask, seqs, spread):
     ok(c.layer)
 
 
+@pytest.mark.parametrize("dtype,H,hk,d,seqs", [
+    ("bf16", 1, 1, 128, [(1, 20001)]), ("bf16", 3, 1, 128, [(1, 9000)]), ("bf16", 16, 2, 128, [(1, 20000)]),
+    ("bf16", 64, 2, 128, [(1, 9001), (2, 300)]), ("bf16", 64, 1, 128, [(1, 20000)]), ("bf16", 10, 1, 128, [(12, 12000)]),
+    ("f32", 2, 1, 32, [(1, 9000)]), ("f32", 24, 1, 64, [(1, 7000)]), ("f32", 8, 1, 128, [(4, 7001), (1, 1)])])
+def test_attend_few_rows_of_a_long_cache(dtype, H, hk, d, seqs):
+    """Items cut into as many pieces as there are CTAs, with few and many rows to join."""
+    c = Paged(dtype, H, hk, d, 16, seqs, 17)
+    q = c.randn(c.T, H, d, scale=3.0)
+    c.to_gpu()
+    o, lse = c.layer.attend(c.batch, q.cuda(), mask_block=1)
+    for _ in range(3):
+        o2, lse2 = c.layer.attend(c.batch, q.cuda(), mask_block=1)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    ok(c.layer)
+    qh = host(q)
+    ref_o, ref_l, mag = po.attend(qh, np.nan_to_num(host(c.kp)), np.nan_to_num(host(c.vp)), seqs, c.tables.numpy(), 1)
+    bo, bl = attend_bounds(dtype, d, *logit_parts(c, qh), c.width, mag, ref_o)
+    assert (np.abs(host(o) - ref_o) <= bo).all()
+    assert (np.abs(host(lse) - ref_l) <= bl).all()
+
+
 def test_attend_weights_sum_to_one_over_long_caches():
     """A cache longer than any tile or page, every CTA's range cut: equal keys give the mean of V."""
     c = Paged("bf16", 8, 2, 128, 64, [(1, 9999), (300, 5000)], 2)
