@@ -24,7 +24,8 @@ LIB_DEBUG = os.path.join(HERE, "libarl2_debug.so")
 SOURCES = ["arl2_api.cu", "attn_pair.cu", "gemm_bf16.cu", "state_bf16.cu", "f32_path.cu", "util.cu", "block.cu", "token_level.cu",
            "paged_api.cu", "paged_prep.cu", "paged_f32.cu", "paged_attn_bf16.cu",
            "paged_weights_bf16.cu", "paged_evict.cu"]
-HEADERS = ["params.h", "layer.h", "paged.h", "paged_join.cuh", "paged_mma.cuh", "sm100.cuh"]
+HEADERS = ["params.h", "layer.h", "paged.h", "paged_join.cuh", "paged_mma.cuh", "paged_weights.cuh",
+           "sm100.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

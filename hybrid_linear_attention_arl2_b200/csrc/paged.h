@@ -90,7 +90,7 @@ struct PagedWeightParams {
   int32_t mask_block;
   FastDiv mask, per_group, per_tile;  // by mask_block, group, a tile's tokens
   float scale_log2;
-  float* part_w;        // bf16: [2 * grid][256] sums of key blocks that CTAs share
+  float* part_w;        // [2 * grid][256, f32 64] sums of key blocks that CTAs share
   uint32_t* joined;     // as PagedAttnParams'
   uint32_t* err;
   uint64_t wait_limit_ns;
@@ -173,7 +173,7 @@ bool paged_query_map(CUtensorMap* m, const void* q, int64_t tokens, int heads, i
 // those on one key head together (PagedWalk::rotation)
 cudaError_t launch_paged_attn_bf16(PagedAttnParams p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                                    bool rotate, cudaStream_t st);
-cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st);
+cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, int sms, cudaStream_t st);
 cudaError_t launch_paged_weights_bf16(const PagedWeightParams& p, const CUtensorMap& tk, int sms, cudaStream_t st);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t st);
 

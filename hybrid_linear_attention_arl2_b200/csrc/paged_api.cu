@@ -495,13 +495,14 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
   p.wait_limit_ns = h->wait_ns;
   p.mask = FastDiv(mask_block);
   p.per_group = FastDiv(p.group);
-  p.per_tile = FastDiv(128 / p.group);
-  if (double(batch->n_seqs) * c.kv_heads * (batch->max_kv / 256 + 1) * (batch->max_q / (128 / p.group) + 1) >= 2147483647.0)
+  const int keys = c.dtype == ARL2_BF16 ? 256 : 64;
+  p.per_tile = FastDiv((c.dtype == ARL2_BF16 ? 128 : 64) / p.group);
+  if (double(batch->n_seqs) * c.kv_heads * (batch->max_kv / keys + 1) * (batch->max_q / p.per_tile.by + 1) >= 2147483647.0)
     return ARL2_ERR_UNSUPPORTED;
   p.part_w = h->part_o;
   p.joined = h->joined;
   PAGED_TRY(c.dtype == ARL2_BF16 ? launch_paged_weights_bf16(p, h->tm_k, h->sms, h->last_stream)
-                                 : launch_paged_weights_f32(p, h->last_stream));
+                                 : launch_paged_weights_f32(p, h->sms, h->last_stream));
   return ARL2_OK;
 }
 

@@ -7,13 +7,22 @@
 // One pass over the keys with the running maximum and sum of each row (Q K^T
 // in units of log2).  A CTA holds 64 query rows (token, head of the group) of
 // one key head and takes tiles of 64 keys; S and O are 4 x 4 and 4 x d/16
-// register tiles a thread, P passes through shared memory.  The f32 path is
-// bound by the FMA pipe: 4 d FMAs a (row, key) pair.
+// register tiles a thread, in packed pairs, P passes through shared memory.  The
+// f32 path is bound by the FMA pipe: 4 d FMAs a (row, key) pair.
+//
+// Tiles come by 16-byte asynchronous copies: V while S is computed, the next K
+// while O is, the page numbers of the tile after a step earlier still.  Tiles of
+// one buffer each, chunks of 16 bytes swizzled in place of padding, leave room
+// for two CTAs an SM with 128 columns, and one's products pass while the other
+// waits.  1000 causal tokens of 4 heads of 128 columns on 5000 keys: 320 us, 29
+// TFLOP/s (541 with tiles loaded between barriers, one CTA an SM); single tokens
+// of 16 heads on 2 key heads over 29300 keys: 103 us (154).
 
 #include <cuda_bf16.h>
 
 #include "paged.h"
 #include "paged_join.cuh"
+#include "paged_weights.cuh"
 #include "params.h"
 #include "sm100.cuh"
 
@@ -24,65 +33,109 @@ namespace {
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
 using Plan = PagedPlan<1, kKeys, 1>;
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+// Copies 16 bytes into shared memory asynchronously; zeros where `there` is false.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Rows of keys [k0, k0 + 64) of stream b and head hk into dst[64][ld] as
-// float; keys at or past `end` and keys of pages that are none read as zeros.
-__device__ __forceinline__ void load_keys(float* dst, int ld, const float* pool, const PagedSeqs& s, int b, int hk,
-                                          int kv_heads, int d, int k0, int end, uint32_t* err) {
-  const int v4 = d >> 2;
-  for (int i = threadIdx.x; i < kKeys * v4; i += kThreads) {
-    const int r = i / v4, c = (i - r * v4) * 4, j = k0 + r;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < end) {
-      const int pg = page_of(s, b, j, err);
-      if (pg >= 0) v = load4(pool + ((int64_t(pg) * kv_heads + hk) * s.page_size + s.page.mod(j)) * d + c);
-    }
-    store4(dst + r * ld + c, v);
+// Columns of a tile's rows in shared memory: whole runs of 8 chunks of 4, since
+// the chunks of K rows are swizzled by row & 7, those of Q by (row >> 2) & 1.
+__host__ __device__ inline int tile_pitch(int d) { return (d + 31) & ~31; }
+
+// How a block's threads copy rows of d columns: a power of two of lanes a row.
+struct Lanes {
+  int shift, chunks;
+  __device__ explicit Lanes(int d) : shift(0), chunks(d >> 2) {
+    while ((1 << shift) < chunks) ++shift;
   }
+  // f(row, chunk) for every 16 bytes of 64 rows
+  template <class F>
+  __device__ __forceinline__ void each(const F& f) const {
+    const int c = threadIdx.x & ((1 << shift) - 1);
+    if (c < chunks)
+      for (int r = threadIdx.x >> shift; r < kKeys; r += kThreads >> shift) f(r, c);
+  }
+};
+
+// The page entry of key j of stream b (of a key behind the last: none), and from
+// it the pool row of head hk; -1 where there is none or the entry is no page (recorded).
+__device__ __forceinline__ int page_entry(const PagedSeqs& s, int b, int j, int end) {
+  return j < end ? s.pages[int64_t(b) * s.pages_ld + s.page.div(j)] : -1;
+}
+__device__ __forceinline__ int pool_row(const PagedSeqs& s, int entry, int hk, int kv_heads, int j, int end, uint32_t* err) {
+  if (j >= end) return -1;
+  if (unsigned(entry) >= unsigned(s.n_pages)) {
+    if (err) atomicCAS(err, 0u, kDevPage);
+    return -1;
+  }
+  return (entry * kv_heads + hk) * s.page_size + s.page.mod(j);
 }
 
-// S = Q K^T for this thread's 4 rows (4 ty ..) x 4 keys (tx + 16 i).
-__device__ __forceinline__ void scores(const float* sQ, const float* sK, int ld, int d, int ty, int tx,
-                                       float (&acc)[4][4]) {
+// Starts the copy of 64 pool rows into a tile; `swizzle`: K's chunks.
+__device__ __forceinline__ void copy_keys(float* dst, const float* pool, const int* rows, const Lanes& lanes, int pitch,
+                                          int d, bool swizzle) {
+  lanes.each([&](int r, int c) {
+    const int row = rows[r];
+    copy16(dst + r * pitch + 4 * (swizzle ? c ^ (r & 7) : c), pool + int64_t(max(row, 0)) * d + 4 * c, row >= 0);
+  });
+}
+
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// S = Q K^T for this thread's 4 rows (4 ty ..) x 4 keys (tx + 16 i), even and odd columns apart.
+__device__ __forceinline__ void scores(const float* sQ, const float* sK, int pitch, int chunks, int ty, int tx,
+                                       float (&out)[4][4]) {
+  float2 acc[4][4];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[a][i] = 0.f;
-  for (int c = 0; c < d; c += 4) {
+    for (int i = 0; i < 4; ++i) acc[a][i] = make_float2(0.f, 0.f);
+  const float* q0 = sQ + 4 * ty * pitch;
+  const float* k0 = sK + tx * pitch;
+  const int xq = ty & 1, xk = tx & 7;
+#pragma unroll 2
+  for (int c = 0; c < chunks; ++c) {
     float4 q[4], k[4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) q[a] = *reinterpret_cast<const float4*>(sQ + (4 * ty + a) * ld + c);
+    for (int a = 0; a < 4; ++a) q[a] = lds4(q0 + a * pitch + 4 * (c ^ xq));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sK + (tx + 16 * i) * ld + c);
+    for (int i = 0; i < 4; ++i) k[i] = lds4(k0 + 16 * i * pitch + 4 * (c ^ xk));
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[a][i] = dot4(q[a], k[i], acc[a][i]);
+      for (int i = 0; i < 4; ++i) {
+        acc[a][i] = __ffma2_rn(make_float2(q[a].x, q[a].y), make_float2(k[i].x, k[i].y), acc[a][i]);
+        acc[a][i] = __ffma2_rn(make_float2(q[a].z, q[a].w), make_float2(k[i].z, k[i].w), acc[a][i]);
+      }
   }
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[a][i] = acc[a][i].x + acc[a][i].y;
 }
 
-__host__ __device__ inline size_t smem_floats(int d) {
-  return size_t(2 * kRows + kKeys) * (d + 4) + size_t(kKeys) * (kRows + 4);
+__host__ __device__ inline size_t attn_smem(int d) {
+  return (size_t(kRows + 2 * kKeys) * tile_pitch(d) + size_t(kKeys) * kRows) * sizeof(float);
 }
+__host__ __device__ inline size_t weights_smem(int d) { return size_t(2 * kRows + kKeys) * tile_pitch(d) * sizeof(float); }
 
 // DC: 64-column chunks of the head dimension a thread accumulates (d <= 64 DC).
 template <int DC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 paged_attn_f32_kernel(const PagedAttnParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
   extern __shared__ float sm[];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = tile_pitch(d);
+  const Lanes lanes(d);
   float* sQ = sm;
   float* sK = sQ + kRows * ld;
   float* sV = sK + kKeys * ld;
-  float* sP = sV + kKeys * ld;  // [key][row], pitch 68
-  constexpr int kPl = kRows + 4;
+  float* sP = sV + kKeys * ld;  // [key][row], chunks of 4 rows swizzled by key & 7
+  __shared__ int pool_rows[2][kKeys];  // of this tile's and the next one's keys
   __shared__ PagedWalk<Plan> walk;
   __shared__ int join, more;
   if (tid < 32) {
@@ -98,36 +151,46 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
   while (more) {
     const PagedSeg<Plan> s = walk.seg;
     const int rows = s.blk.n_tok * p.group, b = p.per_blk.div(s.f);
-    // query rows, and each of this thread's rows' visible keys
-    for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
-      const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows)
-        v = load4(q + int64_t(s.blk.row0 + p.per_group.div(r)) * p.ld_q + (s.hk * p.group + p.per_group.mod(r)) * d + c);
-      store4(sQ + r * ld + c, v);
+    const float* k_pool = static_cast<const float*>(p.k_pool);
+    const float* v_pool = static_cast<const float*>(p.v_pool);
+    // the first keys' pages, query rows, and each of this thread's rows' visible keys
+    if (tid < kKeys) {
+      const int j = s.u0 * kKeys + tid;
+      pool_rows[0][tid] = pool_row(p.s, page_entry(p.s, b, j, s.blk.kv), s.hk, p.kv_heads, j, s.blk.kv, p.err);
     }
+    lanes.each([&](int r, int c) {
+      const int tok = r < rows ? p.per_group.div(r) : 0, head = r < rows ? p.per_group.mod(r) : 0;
+      copy16(sQ + r * ld + 4 * (c ^ ((r >> 2) & 1)), q + int64_t(s.blk.row0 + tok) * p.ld_q + (s.hk * p.group + head) * d + 4 * c,
+             r < rows);
+    });
+    __syncthreads();
+    copy_keys(sK, k_pool, pool_rows[0], lanes, ld, d, true);
+    copy_commit();
     int lim[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = 4 * ty + a;
       lim[a] = r < rows ? visible_keys(s.blk.view(), p.mask, s.blk.t0 + p.per_group.div(r)) : 0;
     }
-    float m[4], l[4], o[4][4 * DC];
+    float m[4], l[4];
+    float2 o[4][2 * DC];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       m[a] = -INFINITY;
       l[a] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4 * DC; ++c) o[a][c] = 0.f;
+      for (int c = 0; c < 2 * DC; ++c) o[a][c] = make_float2(0.f, 0.f);
     }
     for (int j = s.u0; j < s.u1; ++j) {
-      const int k0 = j * kKeys;
-      __syncthreads();
-      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, b, s.hk, p.kv_heads, d, k0, s.blk.kv, p.err);
-      load_keys(sV, ld, static_cast<const float*>(p.v_pool), p.s, b, s.hk, p.kv_heads, d, k0, s.blk.kv, p.err);
-      __syncthreads();
+      const int k0 = j * kKeys, at = (j - s.u0) & 1, ahead = k0 + kKeys + tid;
+      copy_wait();
+      __syncthreads();  // K and Q are there, V and P are read
+      copy_keys(sV, v_pool, pool_rows[at], lanes, ld, d, false);
+      copy_commit();
+      const bool fetch = tid < kKeys && j + 1 < s.u1;
+      const int entry = fetch ? page_entry(p.s, b, ahead, s.blk.kv) : -1;
       float acc[4][4];
-      scores(sQ, sK, ld, d, ty, tx, acc);
+      scores(sQ, sK, ld, d >> 2, ty, tx, acc);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         float mx = -INFINITY;
@@ -152,28 +215,32 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
         l[a] = fmaf(l[a], corr, sum);
         m[a] = mn;
 #pragma unroll
-        for (int c = 0; c < 4 * DC; ++c) o[a][c] *= corr;
+        for (int c = 0; c < 2 * DC; ++c) o[a][c] = __fmul2_rn(o[a][c], make_float2(corr, corr));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(sP + (tx + 16 * i) * kPl + 4 * ty) =
+        *reinterpret_cast<float4*>(sP + (tx + 16 * i) * kRows + 4 * (ty ^ (tx & 7))) =
             make_float4(acc[0][i], acc[1][i], acc[2][i], acc[3][i]);
-      __syncthreads();
-#pragma unroll 4
+      if (fetch) pool_rows[at ^ 1][tid] = pool_row(p.s, entry, s.hk, p.kv_heads, ahead, s.blk.kv, p.err);
+      copy_wait();
+      __syncthreads();  // V, P and the next pages are there, K is read
+      if (j + 1 < s.u1) {
+        copy_keys(sK, k_pool, pool_rows[at ^ 1], lanes, ld, d, true);
+        copy_commit();
+      }
+#pragma unroll 8
       for (int k = 0; k < kKeys; ++k) {
-        const float4 pk = *reinterpret_cast<const float4*>(sP + k * kPl + 4 * ty);
+        const float4 pk = lds4(sP + k * kRows + 4 * (ty ^ (k & 7)));
+        const float pr[4] = {pk.x, pk.y, pk.z, pk.w};
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
           const int col = tx * 4 + 64 * c;
           if (col < d) {
-            const float4 v = *reinterpret_cast<const float4*>(sV + k * ld + col);
-            const float pr[4] = {pk.x, pk.y, pk.z, pk.w};
+            const float4 v = lds4(sV + k * ld + col);
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-              o[a][4 * c] = fmaf(pr[a], v.x, o[a][4 * c]);
-              o[a][4 * c + 1] = fmaf(pr[a], v.y, o[a][4 * c + 1]);
-              o[a][4 * c + 2] = fmaf(pr[a], v.z, o[a][4 * c + 2]);
-              o[a][4 * c + 3] = fmaf(pr[a], v.w, o[a][4 * c + 3]);
+              o[a][2 * c] = __ffma2_rn(make_float2(pr[a], pr[a]), make_float2(v.x, v.y), o[a][2 * c]);
+              o[a][2 * c + 1] = __ffma2_rn(make_float2(pr[a], pr[a]), make_float2(v.z, v.w), o[a][2 * c + 1]);
             }
           }
         }
@@ -194,8 +261,8 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
       for (int c = 0; c < DC; ++c) {
         const int col = tx * 4 + 64 * c;
         if (col >= d) continue;
-        const float4 x = make_float4(o[a][4 * c] * inv, o[a][4 * c + 1] * inv, o[a][4 * c + 2] * inv,
-                                     o[a][4 * c + 3] * inv);
+        const float4 x = make_float4(o[a][2 * c].x * inv, o[a][2 * c].y * inv, o[a][2 * c + 1].x * inv,
+                                     o[a][2 * c + 1].y * inv);
         if (whole)
           store4(static_cast<float*>(p.o) + orow * d + col, x);
         else
@@ -229,67 +296,112 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
 }
 
 // ------------------------------------------------------------------ weights
-// One CTA per (stream, key head, 64 keys): every new token's rows go past in
-// tiles of 64, a thread sums its 4 rows' weights of its 4 keys.
-__global__ void __launch_bounds__(kThreads)
-paged_weights_f32_kernel(const PagedWeightParams p, int n_kt) {
+// A CTA takes its range of key blocks (paged_weights.cuh), 64 keys each, and the
+// new tokens' rows past them in tiles of 64, the next tile's copy under way; a
+// thread sums its 4 rows' weights of its 4 keys.  500 tokens of 8 heads a key
+// head on 500 keys and 400 on 3000, 64 columns: 111 us, 380 with a CTA a block;
+// clusters that shared a block's rows took 144, but 1800 instead of 250 (166 now)
+// where most streams have one token.
+__global__ void __launch_bounds__(kThreads, 2)
+paged_weights_f32_kernel(const PagedWeightParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
   extern __shared__ float sm[];
   __shared__ float part[16][kKeys];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = d + 4;
-  float* sQ = sm;
-  float* sK = sQ + kRows * ld;
+  __shared__ int pool_rows[kKeys];
+  __shared__ WeightWalk<kKeys> walk;
+  __shared__ WeightBlk blk;
+  __shared__ int join;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = p.d, ld = tile_pitch(d);
+  const Lanes lanes(d);
+  float* sK = sm;
+  float* sQ = sK + kKeys * ld;  // two tiles
   const float* q = static_cast<const float*>(p.q);
-  const int qt = kRows / p.group;
-  const long long items = (long long)p.s.n_seqs * p.kv_heads * n_kt;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int jt = int(it % n_kt), hk = int(it / n_kt % p.kv_heads), b = int(it / n_kt / p.kv_heads);
-    const SeqView v = load_seq(p.s, b, p.err);
-    const int k0 = jt * kKeys;
-    if (v.n < 0) continue;
-    float* out = p.w_out + (int64_t(b) * p.kv_heads + hk) * p.w_ld;
-    const float* in = p.w_in + (int64_t(b) * p.kv_heads + hk) * p.w_ld;
-    if (k0 < v.kv) {
-      __syncthreads();
-      load_keys(sK, ld, static_cast<const float*>(p.k_pool), p.s, b, hk, p.kv_heads, d, k0, v.kv, p.err);
-      float w[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int t0 = 0; t0 < v.n; t0 += qt) {
-        const int rows = min(qt, v.n - t0) * p.group;
-        if (visible_keys(v, p.mask, min(t0 + qt, v.n) - 1) <= k0) continue;  // no row of the tile sees the keys
-        __syncthreads();
-        for (int i = tid; i < kRows * (d >> 2); i += kThreads) {
-          const int r = i / (d >> 2), c = (i - r * (d >> 2)) * 4;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < rows) x = load4(q + int64_t(v.q0 + t0 + r / p.group) * p.ld_q + (hk * p.group + r % p.group) * d + c);
-          store4(sQ + r * ld + c, x);
-        }
-        __syncthreads();
-        float acc[4][4];
-        scores(sQ, sK, ld, d, ty, tx, acc);
+  const int qt = p.per_tile.by;  // tokens of a tile
+  if (tid < 32) {
+    WeightWalk<kKeys> mine;
+    mine.find(p);
+    mine.next(p, blk);
+    if (tid == 0) walk = mine;
+  } else {
+    clear_tails(p, int(blockIdx.x) * (kThreads / 32 - 1) + (tid >> 5) - 1, int(gridDim.x) * (kThreads / 32 - 1));
+  }
+  __syncthreads();
+  while (blk.more) {
+    const int k0 = blk.jt * kKeys, hk = blk.hk, b = blk.b, rt1 = blk.rt1;
+    const SeqView v{blk.q0, blk.n, blk.kv};
+    if (tid < kKeys)
+      pool_rows[tid] = pool_row(p.s, page_entry(p.s, b, k0 + tid, v.kv), hk, p.kv_heads, k0 + tid, v.kv, p.err);
+    auto copy_rows = [&](int tile, float* dst) {
+      const int rows = min(qt, v.n - tile * qt) * p.group;
+      lanes.each([&](int r, int c) {
+        const int tok = r < rows ? p.per_group.div(r) : 0, head = r < rows ? p.per_group.mod(r) : 0;
+        copy16(dst + r * ld + 4 * (c ^ ((r >> 2) & 1)),
+               q + int64_t(v.q0 + tile * qt + tok) * p.ld_q + (hk * p.group + head) * d + 4 * c, r < rows);
+      });
+      copy_commit();
+    };
+    copy_rows(blk.rt0, sQ);
+    __syncthreads();
+    copy_keys(sK, static_cast<const float*>(p.k_pool), pool_rows, lanes, ld, d, true);
+    copy_commit();
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    int at = 0;
+    for (int t = blk.rt0; t < rt1; ++t, at ^= 1) {
+      const int rows = min(qt, v.n - t * qt) * p.group;
+      float lse2[4];
+      int lim[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int r = 4 * ty + a;
-          if (r >= rows) continue;
-          const int t = t0 + r / p.group, lim = visible_keys(v, p.mask, t);
-          const float lse = p.lse[int64_t(v.q0 + t) * p.heads + hk * p.group + r % p.group];
-          if (lse == -INFINITY) continue;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (k0 + tx + 16 * i < lim) w[i] += exp2f(fmaf(acc[a][i], p.scale_log2, -1.4426950408889634f * lse));
+      for (int a = 0; a < 4; ++a) {
+        const int r = 4 * ty + a;
+        lim[a] = 0, lse2[a] = 0.f;
+        if (r < rows) {
+          const int tok = t * qt + p.per_group.div(r);
+          const float lse = p.lse[int64_t(v.q0 + tok) * p.heads + hk * p.group + p.per_group.mod(r)];
+          if (lse != -INFINITY) lim[a] = visible_keys(v, p.mask, tok);
+          lse2[a] = -1.4426950408889634f * lse;
         }
       }
+      copy_wait();
+      __syncthreads();  // the tile is there, the one before is read
+      if (t + 1 < rt1) copy_rows(t + 1, sQ + (at ^ 1) * kRows * ld);
+      float acc[4][4];
+      scores(sQ + at * kRows * ld, sK, ld, d >> 2, ty, tx, acc);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[ty][tx + 16 * i] = w[i];
-      __syncthreads();
-      if (tid < kKeys && k0 + tid < v.kv) {
-        float sum = 0.f;
-        for (int y = 0; y < 16; ++y) sum += part[y][tid];
-        out[k0 + tid] = fmaf(p.decay, in[k0 + tid], sum);
-      }
-      __syncthreads();
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k0 + tx + 16 * i < lim[a]) w[i] += exp2f(fmaf(acc[a][i], p.scale_log2, lse2[a]));
     }
-    if (tid < kKeys && k0 + tid >= v.kv && k0 + tid < p.w_ld) out[k0 + tid] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[ty][tx + 16 * i] = w[i];
+    __syncthreads();
+    float sum = 0.f;
+    if (tid < kKeys)
+      for (int y = 0; y < 16; ++y) sum += part[y][tid];
+    bool mine = tid < kKeys;
+    if (blk.pieces > 1) {
+      if (mine) {
+        p.part_w[(2 * blockIdx.x + blk.slot) * kKeys + tid] = sum;
+        __threadfence();
+      }
+      __syncthreads();
+      if (tid == 0) join = last_piece(p.joined + 8 * blk.owner, blk.pieces);
+      __syncthreads();
+      mine = mine && join;
+      if (mine) {
+        sum = __ldcg(&p.part_w[(2 * blk.owner + blk.owner_slot) * kKeys + tid]);
+#pragma unroll 8
+        for (int x = 1; x < blk.pieces; ++x) sum += __ldcg(&p.part_w[2 * (blk.owner + x) * kKeys + tid]);
+      }
+    }
+    if (mine && k0 + tid < v.kv) {
+      const int64_t to = (int64_t(b) * p.kv_heads + hk) * p.w_ld + k0 + tid;
+      p.w_out[to] = fmaf(p.decay, p.w_in[to], sum);
+    }
+    __syncthreads();  // the block is read
+    if (tid == 0) walk.next(p, blk);
+    __syncthreads();
   }
 }
 
@@ -297,10 +409,9 @@ template <int DC>
 cudaError_t launch_attn(PagedAttnParams p, int grid, cudaStream_t st) {
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_attn_f32_kernel<DC>),
-                                   int(smem_floats(128) * sizeof(float)), &done);
+                                   int(attn_smem(128)), &done);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(paged_attn_f32_kernel<DC>, dim3(unsigned(grid)), kThreads, smem_floats(p.d) * sizeof(float), st, 0,
-                           p);
+  return launch_overlapped(paged_attn_f32_kernel<DC>, dim3(unsigned(grid)), kThreads, attn_smem(p.d), st, 0, p);
 }
 
 }  // namespace
@@ -309,16 +420,12 @@ cudaError_t launch_paged_attn_f32(PagedAttnParams p, int grid, cudaStream_t st) 
   return p.d <= 64 ? launch_attn<1>(p, grid, st) : launch_attn<2>(p, grid, st);
 }
 
-cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, cudaStream_t st) {
-  const int bytes = int(size_t(kRows + kKeys) * (p.d + 4) * sizeof(float));
+cudaError_t launch_paged_weights_f32(const PagedWeightParams& p, int sms, cudaStream_t st) {
   static unsigned done = 0;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(paged_weights_f32_kernel),
-                                   int(size_t(kRows + kKeys) * 132 * sizeof(float)), &done);
+                                   int(weights_smem(128)), &done);
   if (e != cudaSuccess) return e;
-  const long long n_kt = (p.w_ld + kKeys - 1) / kKeys;
-  const long long items = n_kt * p.s.n_seqs * p.kv_heads;
-  const unsigned grid = unsigned(items < (1 << 20) ? items : (1 << 20));
-  return launch_overlapped(paged_weights_f32_kernel, dim3(grid), kThreads, size_t(bytes), st, 0, p, int(n_kt));
+  return launch_overlapped(paged_weights_f32_kernel, dim3(2 * unsigned(sms)), kThreads, weights_smem(p.d), st, 0, p);
 }
 
 }  // namespace arl2
