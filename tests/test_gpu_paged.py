@@ -228,6 +228,16 @@ def test_attend_few_rows_of_a_long_cache(dtype, H, hk, d, seqs):
     assert (np.abs(host(lse) - ref_l) <= bl).all()
 
 
+@pytest.mark.parametrize("dtype,H,hk,d,page,mask,seqs", [
+    ("f32", 8, 1, 64, 16, 1, [(600, 700), (1, 3000), (0, 40), (1, 1)]),
+    ("f32", 4, 4, 128, 8, 0, [(300, 300), (257, 90), (1, 1000)]),
+    ("f32", 2, 1, 36, 24, 50, [(900, 64), (130, 130)]),
+    ("bf16", 16, 1, 128, 16, 1, [(500, 600), (1, 5000), (0, 30)])])
+def test_attend_and_weights_of_cut_blocks(dtype, H, hk, d, page, mask, seqs):
+    """Chunks whose blocks of keys several CTAs share, beside streams of one token and of none."""
+    test_attend_and_weights(dtype, H, hk, d, page, mask, seqs, 2.0)
+
+
 def test_attend_weights_sum_to_one_over_long_caches():
     """A cache longer than any tile or page, every CTA's range cut: equal keys give the mean of V."""
     c = Paged("bf16", 8, 2, 128, 64, [(1, 9999), (300, 5000)], 2)
