@@ -68,7 +68,7 @@ struct PagedAttnParams {
   FastDiv mask, per_group, per_blk;  // by mask_block, group, n_qblk
   float scale_log2;     // softmax scale * log2(e)
   // work division (see PagedPlan): tokens of a tile, blocks of query rows per stream at most
-  int32_t qt, n_qblk;
+  int32_t qt, n_qblk, min_cost;
   float* part_o;        // [2 * grid][rows][d] pieces of items that several CTAs share
   float2* part_ml;      // [2 * grid][rows] their running max (log2 units) and sum
   uint32_t* joined;     // [grid][8] pieces of a CTA's cut item that are in (a count for each warp's rows); zero between launches
@@ -236,7 +236,8 @@ __device__ __forceinline__ int visible_keys(const SeqView& v, const FastDiv& mas
 // cut by a range's end is finished from the CTAs' pieces by the one that comes
 // last: a CTA has at most two, one at its range's begin (slot 0) and one at its
 // end (slot 1).  An item has at least one unit, so that rows which see no key get
-// their zeros.  (The launch bounds the units below 2^31.)
+// their zeros.  A range costs min_cost at least.  (The launch bounds the units
+// below 2^31.)
 template <int kTiles, int kKeys, int kItemCost_>
 struct PagedPlan {
   static constexpr int kItemCost = kItemCost_;
@@ -309,7 +310,7 @@ struct PagedWalk {
       mine += cost_of(blk, p.kv_heads);
     }
     total = __reduce_add_sync(0xffffffffu, mine);
-    const int ctas = min(total, grid);
+    const int ctas = min((total + p.min_cost - 1) / p.min_cost, grid);
     at = end = used = 0;
     have = fresh = true;
     if (cta >= ctas) return;

@@ -438,6 +438,17 @@ arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, con
   p.wait_limit_ns = h->wait_ns;
   if (!paged_plan(p, c.dtype == ARL2_BF16 ? 128 : 64, c.dtype == ARL2_BF16 ? 2 : 1, c.dtype == ARL2_BF16 ? 128 : 64))
     return ARL2_ERR_UNSUPPORTED;
+  // Units of a range at least: one of 256 keys takes about 1.5 us, a piece more in
+  // the join 0.09 for every 8 rows, so that sqrt(0.06 units rows / 8) a range costs
+  // least.  16 tokens of 8 heads a key head on 3000 keys take 31 us (47 with one at
+  // least), one on 20000 keys 24 (28); one token of a head of its own on 1561 keys
+  // 16, and 17.2 with two.  (float32's join is a whole block's: one.)
+  p.min_cost = 1;
+  if (c.dtype == ARL2_BF16) {
+    const int rows = (batch->max_q < p.qt ? batch->max_q : p.qt) * p.group;
+    p.min_cost = int(std::sqrt(0.06 * (batch->max_kv / 256 + 1) * ((rows + 7) / 8)));
+    if (p.min_cost < 1) p.min_cost = 1;
+  }
   // Several blocks of rows on the keys of a pool that L2 does not hold: a frame of
   // 1560 tokens on 201 MB reads 504 MB from memory instead of 945, 402 us instead
   // of 419.  With 33 MB of keys the rotation costs 7 %.

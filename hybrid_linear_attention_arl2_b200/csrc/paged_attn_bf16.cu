@@ -604,7 +604,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
       asked ^= 1u << at;
       const int n = (rows + 3) >> 2;
       if (uniform(*const_cast<const volatile int*>(&s->last) != 0 && quarter * n < rows))
-        join_rows<__nv_bfloat16, 256, true>(p, s->owner, s->owner_slot, s->pieces, quarter * n, min(n, rows - quarter * n),
+        join_rows(p, s->owner, s->owner_slot, s->pieces, quarter * n, min(n, rows - quarter * n),
                                             out_row);
     }
     if (join) {  // O_1 and its statistics are read

@@ -1,7 +1,7 @@
 // Joins the pieces of an attention item that several CTAs share (paged.h's work
-// division), for the float32 and the bf16 kernel: with M the largest of their
-// maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, in key order whoever
-// joins them.  The CTA that comes last does it, told by a count; nobody waits.
+// division): with M the largest of their maxima, O = sum 2^(m_i - M) O_i /
+// sum 2^(m_i - M) l_i, in the same order whoever joins them.  The CTA that comes
+// last does it, told by a count; nobody waits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,15 +33,15 @@ __device__ __forceinline__ int64_t piece_at(int64_t first, int row, int col8) {
   return first * 128 + (col8 * 256 + row) * 8;
 }
 
-// Rows [r0, r0 + n) of a piece's kPieceRows, n <= 32, by one warp: the lanes
-// hold the rows' statistics; then kRows rows at a time, a lane's four columns
-// each, kUnroll pieces in flight.  `out(r)`: row r's index in O's [token, head] rows.  kLanes: the piece
-// is laid out for a thread a row (piece_at), else row by row.
-template <typename T, int kPieceRows, bool kLanes, int kRows, int kUnroll, class Out>
+// bf16: rows [r0, r0 + n) of the pieces' 256 (piece_at), n <= 32, by one warp: the
+// lanes hold the rows' statistics; then kRows rows at a time, a lane's four
+// columns each, kUnroll pieces in flight.  `out(r)`: row r's index in O's [token,
+// head] rows.
+template <int kRows, int kUnroll, class Out>
 __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
                                           const Out& out) {
-  const int lane = threadIdx.x & 31, d = p.d;
-  auto piece = [&](int k) { return int64_t(k == 0 ? 2 * owner + owner_slot : 2 * (owner + k)) * kPieceRows + r0; };
+  const int lane = threadIdx.x & 31;
+  auto piece = [&](int k) { return int64_t(k == 0 ? 2 * owner + owner_slot : 2 * (owner + k)) * 256 + r0; };
   float M = -INFINITY, L = 0.f;
   if (kRows == 2) {  // the lanes share the pieces, 32 at a time
     float mine[2] = {-INFINITY, -INFINITY};
@@ -78,9 +78,9 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i0 + i < n && lane * 4 < d && k0 + u < pieces)
+          if (i0 + i < n && k0 + u < pieces)
             v[u][i] = __ldcg(reinterpret_cast<const float4*>(
-                p.part_o + (kLanes ? piece_at(at - r0, r0 + i0 + i, lane >> 1) + (lane & 1) * 4 : (at + i0 + i) * d + lane * 4)));
+                p.part_o + piece_at(at - r0, r0 + i0 + i, lane >> 1) + (lane & 1) * 4));
         }
       }
 #pragma unroll
@@ -99,8 +99,8 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const float inv = __shfl_sync(0xffffffffu, rcp, (i0 + i) & 31);
-      if (i0 + i < n && lane * 4 < d)
-        store4(static_cast<T*>(p.o) + out(r0 + i0 + i) * d + lane * 4,
+      if (i0 + i < n)
+        store4(static_cast<__nv_bfloat16*>(p.o) + out(r0 + i0 + i) * 128 + lane * 4,
                make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
     }
   }
@@ -110,13 +110,13 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
 // The same, with more pieces in flight where the rows are few: one token of 16
 // heads on 20000 keys (74 pieces a key head) took 90 us when one warp joined
 // all rows, four pieces' statistics and two pieces' rows at a time; 28 us so.
-template <typename T, int kPieceRows, bool kLanes, class Out>
+template <class Out>
 __device__ __forceinline__ void join_rows(const PagedAttnParams& p, int owner, int owner_slot, int pieces, int r0, int n,
                                           const Out& out) {
   if (n <= 2)
-    join_some<T, kPieceRows, kLanes, 2, 8>(p, owner, owner_slot, pieces, r0, n, out);
+    join_some<2, 8>(p, owner, owner_slot, pieces, r0, n, out);
   else
-    join_some<T, kPieceRows, kLanes, 8, 2>(p, owner, owner_slot, pieces, r0, n, out);
+    join_some<8, 2>(p, owner, owner_slot, pieces, r0, n, out);
 }
 
 }  // namespace arl2
