@@ -565,6 +565,8 @@ def _token_rows(d, dtype, index, tensors):
         return 0, tokens
     if ld < 0:
         raise ValueError("strided views must have one pitch")
+    if ld < max(h for _, _, h in tensors) * d:  # (0, of a view broadcast over tokens, would read as contiguous)
+        raise ValueError(f"token rows {ld} elements apart overlap")
     return ld, tokens
 
 
