@@ -538,6 +538,10 @@ def _bad_rows(name, t, h, d, dtype, index):
                       f"{list(t.shape)} of {t.dtype} on {t.device} with strides {list(t.stride())}")
 
 
+def _not_on_gpu(name, t):
+    return ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+
+
 def _token_rows(d, dtype, index, tensors):
     """The common pitch of [tokens, heads, head_dim] views in elements (0: each
     contiguous), and their tokens, of (name, tensor, heads) triples; raises where
@@ -618,6 +622,8 @@ def qk_norm_rope(prep: QKPrep, q, k, pos=None, q_out=None, k_out=None, stream=No
     import torch
     tokens, h, d = q.shape
     hk, dtype, index = k.shape[1], q.dtype, q.get_device()
+    if index < 0:
+        raise _not_on_gpu("q", q)
     ld, tokens = _token_rows(d, dtype, index, (("q", q, h), ("k", k, hk)))
     prep._check(d, dtype, index, tokens, pos)
     q_out = torch.empty((tokens, h, d), dtype=dtype, device=q.device) if q_out is None else q_out
@@ -674,6 +680,8 @@ class PagedKVLayer:
         self.dtype, self.device, self.index = _torch_dtype(dtype), k_pool.device, k_pool.get_device()
         if k_pool.dim() != 4 or k_pool.shape[1] != kv_heads or k_pool.shape[3] != head_dim:
             raise ValueError("k_pool: expected [n_pages, kv_heads, page_size, head_dim]")
+        if self.index < 0:
+            raise _not_on_gpu("k_pool", k_pool)
         _plain("k_pool", k_pool, self.dtype, self.index)
         _plain("v_pool", v_pool, self.dtype, self.index, k_pool.shape)
         self.k_pool, self.v_pool = k_pool, v_pool

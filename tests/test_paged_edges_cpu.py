@@ -29,3 +29,19 @@ def test_rows_broadcast_over_tokens_are_refused():
         _rows(k=wide.as_strided((6, 1, 8), (16, 8, 1)), q=wide.as_strided((6, 4, 8), (16, 8, 1)))
     # a view of one row for all tokens beside a strided one of the same pitch
     assert _rows(q=wide.as_strided((6, 4, 8), (96, 8, 1)), k=wide.as_strided((6, 1, 8), (96, 8, 1), 32)) == (96, 6)
+
+
+def test_host_tensors_are_refused(monkeypatch):
+    """The library takes device memory: tensors of the host never reach it."""
+    def reached(*a):
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(arl2, "load_library", reached)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    q, pool = torch.zeros(3, 4, 8), torch.zeros(2, 4, 8, 8)
+    for kw in ({}, dict(q_out=torch.empty_like(q), k_out=torch.empty_like(q))):
+        with pytest.raises(ValueError):
+            arl2.qk_norm_rope(arl2.QKPrep([]), q, q, **kw)
+    with pytest.raises(ValueError):
+        arl2.PagedKVLayer(4, 4, 8, arl2.ARL2_F32, pool, pool.clone())
