@@ -575,12 +575,17 @@ arl2_status arl2_paged_last_error(arl2_paged_t h) {
   if (!live(h)) return ARL2_ERR_INVALID_ARGUMENT;
   Device dev(h->device);
   if (!dev.ok) return ARL2_ERR_CUDA;
-  PAGED_TRY(cudaStreamSynchronize(h->last_stream));
+  // the whole device: a captured call's replays run on streams that the handle never saw
+  PAGED_TRY(cudaDeviceSynchronize());
   uint32_t w = 0;
   PAGED_TRY(cudaMemcpy(&w, h->err, sizeof(w), cudaMemcpyDeviceToHost));
-  if (w) {  // (a kernel that gave up may have left pieces counted)
+  if (w) {
+    // A kernel that gave up may have left pieces counted.  A memset of device memory may
+    // return before it has run, and not every stream waits for the default one: it is
+    // waited for here, so that no later launch meets it.
     PAGED_TRY(cudaMemset(h->err, 0, sizeof(w)));
     PAGED_TRY(cudaMemset(h->joined, 0, joined_bytes(h)));
+    PAGED_TRY(cudaStreamSynchronize(nullptr));
   }
   return static_cast<arl2_status>(w);
 }

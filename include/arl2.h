@@ -361,8 +361,11 @@ arl2_status arl2_paged_evict(arl2_paged_t h, const arl2_paged_batch* batch, cons
                              int32_t budget, int32_t sink, int32_t recent, const int32_t* dst_pages, int32_t dst_ld,
                              float* w_out, int32_t* kept, int32_t* kv_len_out, void* stream);
 
-/* Synchronise the handle's last stream and return (and clear) the first error
- * recorded by its kernels (ARL2_ERR_PAGE, ARL2_ERR_TIMEOUT), ARL2_OK if none. */
+/* Wait for the handle's device, whatever streams its calls and the replays of
+ * captured ones ran on, and return (and clear) the first error recorded by its
+ * kernels (ARL2_ERR_PAGE, ARL2_ERR_TIMEOUT), ARL2_OK if none.  After
+ * ARL2_ERR_TIMEOUT a call's outputs are undefined, and so are those of later
+ * calls until this one has returned. */
 arl2_status arl2_paged_last_error(arl2_paged_t h);
 int64_t arl2_paged_device_bytes(arl2_paged_t h);
 /* As arl2_state_set_wait_limit. */

@@ -1,0 +1,86 @@
+"""The paged-cache calls at the edge of what their documentation allows: other
+streams and replays, waits that run out, streams that are left out, queries
+that are no numbers, bounds that are far above the work."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from hybrid_linear_attention_arl2_b200 import arl2, build
+from oracle import paged_oracle as po
+from tests.paged_util import ABI, TORCH, Paged, attend_bounds, host
+
+pytestmark = pytest.mark.gpu
+ERR_TIMEOUT, ERR_PAGE = 5, 9
+DELAY = 200_000_000  # clocks, a tenth of a second
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    arl2.load_library()
+
+
+# ------------------------------------------------------------------ errors
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 32)])
+def test_last_error_waits_for_a_replay_on_another_stream(dtype, d):
+    """A replay runs on a stream that the handle never saw; its error is there when last_error returns."""
+    c = Paged(dtype, 4, 2, d, 16, [(3, 40), (1, 300)], 3).to_gpu()
+    q = c.randn(c.T, 4, d).cuda()
+    o, lse = c.layer.attend(c.batch, q)
+    good = o.clone(), lse.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.layer.attend(c.batch, q, o=o, lse=lse)
+    side = torch.cuda.Stream()
+    c.batch.pages[0, 1] = 10 ** 6
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(DELAY)
+        g.replay()
+    assert c.layer.last_error() == ERR_PAGE and c.layer.last_error() == 0
+    c.batch.pages.copy_(c.tables)
+    torch.cuda.synchronize()
+    for _ in range(20):  # right after an error was cleared, on a stream that does not order with the default one
+        with torch.cuda.stream(side):
+            c.batch.pages[0, 1] = -1
+            c.layer.attend(c.batch, q)
+            c.batch.pages.copy_(c.tables)
+            assert c.layer.last_error() == ERR_PAGE
+            o2, lse2 = c.layer.attend(c.batch, q)
+            assert torch.equal(o2, good[0]) and torch.equal(lse2, good[1])
+    assert c.layer.last_error() == 0
+
+
+def test_waits_that_run_out():
+    """A batch of so many empty streams that finding a CTA's work takes far longer than the limit: the roles that wait
+    for it give up, the kernels return and say so, and after last_error the handle's next results are those of a fresh
+    one."""
+    c = Paged("bf16", 16, 2, 128, 16, [(1, 900), (200, 700), (40, 300)], 19).to_gpu()
+    empty = 20000
+    q_start = torch.cat([c.q_start, c.q_start[-1:].expand(empty)]).cuda()
+    kv_len = torch.cat([c.kv_len, torch.zeros(empty, dtype=torch.int32)]).cuda()
+    pages = torch.cat([c.tables, torch.full((empty, c.tables.shape[1]), -1, dtype=torch.int32)]).cuda()
+    long = arl2.PagedBatch(q_start, kv_len, pages, tokens=c.T, max_q=200, max_kv=900)
+    q = c.randn(c.T, 16, 128).cuda()
+    w = torch.zeros(3 + empty, 2, 900, device="cuda")
+    o, lse = c.layer.attend(long, q, mask_block=1)
+    ref = o, lse, c.layer.weights(long, q, lse, w, mask_block=1)
+    assert c.layer.last_error() == 0
+    for limit in (1000, 10000, 100000, 1000000):
+        for call in (lambda: c.layer.attend(long, q, mask_block=1),
+                     lambda: c.layer.weights(long, q, lse, w, mask_block=1)):
+            arl2.arl2_paged_set_wait_limit(c.layer.handle, limit)
+            call()
+            status = c.layer.last_error()
+            assert status in (0, ERR_TIMEOUT) and c.layer.last_error() == 0
+            assert status == ERR_TIMEOUT or limit > 1000
+            arl2.arl2_paged_set_wait_limit(c.layer.handle, 0)
+            o, l2 = c.layer.attend(long, q, mask_block=1)
+            got = o, l2, c.layer.weights(long, q, lse, w, mask_block=1)
+            assert c.layer.last_error() == 0
+            for x, y in zip(got, ref):
+                assert torch.equal(x, y)
