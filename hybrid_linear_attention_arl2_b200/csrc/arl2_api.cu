@@ -643,17 +643,30 @@ arl2_status arl2_state_set(arl2_state_t h, const float* src, int64_t frame, void
   return ARL2_OK;
 }
 
+// The error word, cleared once it is read.  The whole device is waited for: a
+// captured call's replays run on streams that the handle never saw.
+static arl2_status take_error(int device, uint32_t* err, unsigned* ready, int sms) {
+  int prev = device;
+  ARL2_TRY(cudaGetDevice(&prev));
+  if (prev != device) ARL2_TRY(cudaSetDevice(device));
+  uint32_t w = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&w, err, sizeof(w), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && w) {
+    // A kernel that gave up may have left partial-ready flags raised.  A memset of
+    // device memory may return before it has run, and not every stream waits for the
+    // default one: it is waited for here, so that no later launch meets it.
+    e = cudaMemset(err, 0, sizeof(w));
+    if (e == cudaSuccess && ready) e = cudaMemset(ready, 0, attn_ready_words(sms) * sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  }
+  if (prev != device) cudaSetDevice(prev);
+  return e == cudaSuccess ? static_cast<arl2_status>(w) : from_cuda(e);
+}
+
 arl2_status arl2_last_error(arl2_state_t h) {
   if (!live(h, kStateMagic)) return ARL2_ERR_INVALID_ARGUMENT;
-  ARL2_TRY(cudaStreamSynchronize(h->last_stream));
-  uint32_t w = 0;
-  ARL2_TRY(cudaMemcpy(&w, h->err, sizeof(w), cudaMemcpyDeviceToHost));
-  if (w) {
-    // a kernel that gave up may have left partial-ready flags raised
-    ARL2_TRY(cudaMemset(h->err, 0, sizeof(w)));
-    if (h->attn_ready) ARL2_TRY(cudaMemset(h->attn_ready, 0, attn_ready_words(h->sms) * sizeof(unsigned)));
-  }
-  return static_cast<arl2_status>(w);
+  return take_error(h->device, h->err, h->attn_ready, h->sms);
 }
 
 int64_t arl2_state_device_bytes(arl2_state_t h) { return live(h, kStateMagic) ? h->bytes : -1; }
@@ -852,15 +865,7 @@ int64_t arl2_kv_device_bytes(arl2_kv_t h) { return live(h, kKvMagic) ? h->bytes 
 
 arl2_status arl2_kv_last_error(arl2_kv_t h) {
   if (!live(h, kKvMagic)) return ARL2_ERR_INVALID_ARGUMENT;
-  ARL2_TRY(cudaStreamSynchronize(h->last_stream));
-  uint32_t w = 0;
-  ARL2_TRY(cudaMemcpy(&w, h->err, sizeof(w), cudaMemcpyDeviceToHost));
-  if (w) {
-    // a kernel that gave up may have left partial-ready flags raised
-    ARL2_TRY(cudaMemset(h->err, 0, sizeof(w)));
-    if (h->attn_ready) ARL2_TRY(cudaMemset(h->attn_ready, 0, attn_ready_words(h->sms) * sizeof(unsigned)));
-  }
-  return static_cast<arl2_status>(w);
+  return take_error(h->device, h->err, h->attn_ready, h->sms);
 }
 
 arl2_status arl2_kv_destroy(arl2_kv_t h) {

@@ -163,8 +163,9 @@ arl2_status arl2_state_get(arl2_state_t h, float* dst, int64_t* frame, void* str
  * set the frame counter: checkpoint / resume of a stream. */
 arl2_status arl2_state_set(arl2_state_t h, const float* src, int64_t frame, void* stream);
 
-/* Synchronise the handle's last stream and return (and clear) the first error
- * recorded by its kernels, ARL2_OK if none. */
+/* Wait for the handle's device, whatever streams its calls and the replays of
+ * captured ones ran on, and return (and clear) the first error recorded by its
+ * kernels, ARL2_OK if none. */
 arl2_status arl2_last_error(arl2_state_t h);
 
 /* Device bytes held by the handle.  Fixed at init and independent of the
