@@ -314,6 +314,8 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
   if (e == cudaSuccess) e = cudaMemsetAsync(h->joined, 0, joined_bytes(h), h->last_stream);
   if (e == cudaSuccess) e = device_alloc(reinterpret_cast<void**>(&h->err), 256);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 256, h->last_stream);
+  // the first call may come on a stream that does not wait for this one
+  if (e == cudaSuccess) e = cudaStreamSynchronize(h->last_stream);
   if (e != cudaSuccess) {
     free_paged(h);
     return status_of_cuda(e);

@@ -296,6 +296,7 @@ typedef struct {
 
 typedef struct arl2_paged* arl2_paged_t;
 
+/* Waits for the stream: what it clears is clear for any stream's first call. */
 arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_pool, void* stream,
                             arl2_paged_t* out);
 

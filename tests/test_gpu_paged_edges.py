@@ -84,3 +84,19 @@ def test_waits_that_run_out():
             assert c.layer.last_error() == 0
             for x, y in zip(got, ref):
                 assert torch.equal(x, y)
+
+
+def test_a_new_layer_is_ready_on_any_stream():
+    """What a layer's creation clears is clear when it returns: a call on another stream records its error after it."""
+    c = Paged("bf16", 4, 2, 128, 16, [(3, 40), (1, 300)], 4).to_gpu()
+    q = c.randn(c.T, 4, 128).cuda()
+    c.batch.pages[0, 1] = 10 ** 6
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(DELAY)
+        layer = arl2.PagedKVLayer(4, 2, 128, arl2.ARL2_BF16, c.kp, c.vp)
+    with torch.cuda.stream(b):
+        layer.attend(c.batch, q)
+    torch.cuda.synchronize()
+    assert layer.last_error() == ERR_PAGE
