@@ -73,8 +73,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(const PagedEvict
   const int b = item / p.kv_heads, hk = item - b * p.kv_heads;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int kv = load_kv_len(p.s, b, p.err);
-  if (kv < 0) return;  // (the whole cluster)
+  const int kv = max(0, load_kv_len(p.s, b, p.err));  // (a stream that breaks a bound has no keys afterwards)
   const int64_t row = int64_t(b) * p.kv_heads + hk;
   const float* w = p.w_in + row * p.w_ld;
   float* wo = p.w_out + row * p.w_ld;

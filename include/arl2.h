@@ -270,9 +270,9 @@ arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t h
  * The host gives bounds that size the launches: tokens (rows of the new-token
  * tensors), max_q and max_kv (at least any stream's new tokens and kv_len).
  * What the kernels find out of range they do not access: a stream whose rows
- * or lengths break a bound is left out (its outputs stay as they were), a page
- * number outside [0, n_pages) reads as zeros and is not written; both record
- * ARL2_ERR_PAGE for arl2_paged_last_error. */
+ * or lengths break a bound is left out (its outputs stay as they were, but for
+ * arl2_paged_evict's), a page number outside [0, n_pages) reads as zeros and is
+ * not written; both record ARL2_ERR_PAGE for arl2_paged_last_error. */
 typedef struct {
   int32_t heads;        /* H query heads */
   int32_t kv_heads;     /* Hk: divides heads; heads / kv_heads <= 64 */
@@ -356,6 +356,8 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
  *                shares no byte with w_in.
  *   kept       : int32 [n_seqs, Hk, budget]: the kept keys' old indices, then -1.
  *   kv_len_out : int32 [n_seqs]: min(kv_len, budget).
+ * A stream whose length breaks a bound (ARL2_ERR_PAGE) has no keys afterwards:
+ * its kv_len_out is 0, its kept -1 and its w_out 0.
  * No output shares a byte with an input, another output or the batch's arrays.
  * q_start, tokens and max_q of the batch are not used.
  * budget >= 1, sink and recent >= 0, sink + recent <= budget. */

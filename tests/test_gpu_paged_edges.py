@@ -100,3 +100,29 @@ def test_a_new_layer_is_ready_on_any_stream():
         layer.attend(c.batch, q)
     torch.cuda.synchronize()
     assert layer.last_error() == ERR_PAGE
+
+
+# ------------------------------------------------------------------ streams that are left out
+@pytest.mark.parametrize("bad", ["negative", "bound", "table"])
+def test_eviction_empties_a_stream_that_it_leaves_out(bad):
+    """A stream whose length breaks a bound has no keys afterwards, whatever the outputs' memory held; the others are
+    cut as ever."""
+    kvs, budget = [30, 90, 25], 20
+    c = Paged("f32", 2, 2, 32, 16, [(0, kv) for kv in kvs], 6, dst=[20, 20, 20]).to_gpu()
+    w = torch.rand(3, 2, c.width + 7, generator=c.g).cuda()
+    want = [x.clone() for x in c.layer.evict(c.batch, w, c.dst.cuda(), budget=budget, sink=2, recent=3)]
+    assert c.layer.last_error() == 0
+    c.batch.kv_len[1] = {"negative": -3, "bound": 91, "table": 97}[bad]
+    if bad == "table":
+        c.batch.struct.max_kv = c.width + 7
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    dirty = [torch.full((3, 2, c.width + 7), 5.0, device="cuda"), torch.full((3, 2, budget), 5, dtype=torch.int32, device="cuda"),
+             torch.full((3,), 5, dtype=torch.int32, device="cuda")]
+    del dirty
+    kv_len, w_out, kept = c.layer.evict(c.batch, w, c.dst.cuda(), budget=budget, sink=2, recent=3)
+    assert c.layer.last_error() == ERR_PAGE
+    assert kv_len.tolist() == [20, 0, 20]
+    assert (kept[1] == -1).all() and not w_out[1].any()
+    for got, ref in zip((kv_len, w_out, kept), want):
+        assert torch.equal(got[[0, 2]], ref[[0, 2]])
