@@ -166,13 +166,13 @@ struct WeightWalk {
 
 // What no new token adds to: rows past kv_len are cleared, and the weights of
 // streams without new tokens fade.  Runs of kTail weights, a warp each: `warp` of
-// `warps`.
+// `warps`.  err: null where the caller's division records what breaks a bound.
 constexpr int kTail = 1024;
-__device__ __forceinline__ void clear_tails(const PagedWeightParams& p, int warp, int warps) {
+__device__ __forceinline__ void clear_tails(const PagedWeightParams& p, int warp, int warps, uint32_t* err = nullptr) {
   const long long per_row = (p.w_ld + kTail - 1) / kTail, items = per_row * p.s.n_seqs * p.kv_heads;
   for (long long it = warp; it < items; it += warps) {
     const long long row = it / per_row, j0 = (it - row * per_row) * kTail, j1 = min((long long)p.w_ld, j0 + kTail);
-    const SeqView v = load_seq(p.s, int(row / p.kv_heads), nullptr);
+    const SeqView v = load_seq(p.s, int(row / p.kv_heads), err);
     if (v.n < 0 || (j1 <= v.kv && v.n > 0)) continue;
     const int64_t base = row * p.w_ld;
     for (long long j = j0 + (threadIdx.x & 31); j < j1; j += 32) {

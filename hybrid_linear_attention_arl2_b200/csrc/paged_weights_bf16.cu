@@ -367,7 +367,7 @@ paged_weights_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid
 __global__ void __launch_bounds__(256) paged_weights_fade_kernel(const PagedWeightParams p) {
   grid_dependency_wait();
   allow_dependent_launch();
-  clear_tails(p, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
+  clear_tails(p, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, p.err);
 }
 
 }  // namespace

@@ -126,3 +126,20 @@ def test_eviction_empties_a_stream_that_it_leaves_out(bad):
     assert (kept[1] == -1).all() and not w_out[1].any()
     for got, ref in zip((kv_len, w_out, kept), want):
         assert torch.equal(got[[0, 2]], ref[[0, 2]])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 32)])
+def test_fading_records_streams_that_it_leaves_out(dtype, d):
+    """Weights without new tokens fade; a stream that breaks a bound is left as it was, and said so."""
+    c = Paged(dtype, 4, 2, d, 16, [(0, 40), (0, 70)], 5).to_gpu(max_q=0)
+    q, lse = c.randn(0, 4, d).cuda(), torch.zeros(0, 4, device="cuda")
+    w = torch.rand(2, 2, c.width + 3, generator=c.g).cuda()
+    want = w * 0.5
+    want[0, :, 40:], want[1, :, 70:] = 0, 0
+    assert torch.equal(c.layer.weights(c.batch, q, lse, w, decay=0.5), want)
+    assert c.layer.last_error() == 0
+    c.batch.kv_len[0] = c.width + 1
+    out = torch.full_like(w, 3.0)
+    c.layer.weights(c.batch, q, lse, w, decay=0.5, w_out=out)
+    assert c.layer.last_error() == ERR_PAGE
+    assert (out[0] == 3).all() and torch.equal(out[1], want[1])
