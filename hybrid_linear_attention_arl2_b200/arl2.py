@@ -588,6 +588,19 @@ def _stream_of(index, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """An output that a call on `stream` writes: from that stream's memory, since a block that the current stream gave
+    back may still have writes of its own to come."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream_of(None, stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class QKPrep:
     """Norm and rotation of queries and keys: norm weights (None, None: no
     norm) and up to three position axes."""
@@ -618,7 +631,8 @@ class QKPrep:
 
 def qk_norm_rope(prep: QKPrep, q, k, pos=None, q_out=None, k_out=None, stream=None):
     """Norm and rotate queries [tokens, heads, d] and keys [tokens, kv_heads, d]
-    (views of one pitch, or contiguous) in one pass; returns (q_out, k_out)."""
+    (views of one pitch, or contiguous) in one pass; returns (q_out, k_out).
+    Streams as PagedKVLayer's."""
     import torch
     tokens, h, d = q.shape
     hk, dtype, index = k.shape[1], q.dtype, q.get_device()
@@ -626,8 +640,8 @@ def qk_norm_rope(prep: QKPrep, q, k, pos=None, q_out=None, k_out=None, stream=No
         raise _not_on_gpu("q", q)
     ld, tokens = _token_rows(d, dtype, index, (("q", q, h), ("k", k, hk)))
     prep._check(d, dtype, index, tokens, pos)
-    q_out = torch.empty((tokens, h, d), dtype=dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((tokens, hk, d), dtype=dtype, device=q.device) if k_out is None else k_out
+    q_out = _empty((tokens, h, d), dtype, q.device, stream) if q_out is None else q_out
+    k_out = _empty((tokens, hk, d), dtype, q.device, stream) if k_out is None else k_out
     ld_out, n = _token_rows(d, dtype, index, (("q_out", q_out, h), ("k_out", k_out, hk)))
     if n != tokens:
         raise ValueError("outputs: as many tokens as the inputs")
@@ -672,7 +686,15 @@ class PagedBatch:
 
 class PagedKVLayer:
     """A softmax layer on a paged KV cache (a handle of the C ABI).  The pools
-    are [n_pages, kv_heads, page_size, head_dim]; the layer keeps them alive."""
+    are [n_pages, kv_heads, page_size, head_dim]; the layer keeps them alive.
+
+    Calls run on the current stream, or on ``stream`` (a torch stream or its raw
+    number): its work so far must include what the inputs need, and it may read
+    and write them until it has passed the call.  Outputs that a call allocates
+    belong to that stream: another one waits for it before it reads them, and
+    ``record_stream`` tells the allocator where they are used last.  Rows that
+    belong to no stream of the batch, and streams that the library leaves out
+    (``last_error``), leave an output of attend, weights or append as it was."""
 
     def __init__(self, heads, kv_heads, head_dim, dtype, k_pool, v_pool, *, softmax_scale=0.0, stream=None):
         import torch
@@ -700,7 +722,6 @@ class PagedKVLayer:
     def append(self, batch, k, v, *, q=None, prep=None, pos=None, q_out=None, stream=None):
         """Store the new tokens' K and V; with a prep, K normed and rotated, and
         q's turned rows are returned (q_out)."""
-        import torch
         if q is None:
             if q_out is not None:
                 raise ValueError("q_out without q")
@@ -710,7 +731,7 @@ class PagedKVLayer:
                 raise ValueError("q without a prep")
             ld = self._rows(batch, ("q", q, self.heads), ("k", k, self.kv_heads), ("v", v, self.kv_heads))
             if q_out is None:
-                q_out = torch.empty((batch.tokens, self.heads, self.head_dim), dtype=self.dtype, device=self.device)
+                q_out = _empty((batch.tokens, self.heads, self.head_dim), self.dtype, self.device, stream)
             elif self._rows(batch, ("q_out", q_out, self.heads)):
                 raise ValueError("q_out must be contiguous")
         if prep is not None:
@@ -724,11 +745,11 @@ class PagedKVLayer:
         import torch
         ld = self._rows(batch, ("q", q, self.heads))
         if o is None:
-            o = torch.empty((batch.tokens, self.heads, self.head_dim), dtype=self.dtype, device=self.device)
+            o = _empty((batch.tokens, self.heads, self.head_dim), self.dtype, self.device, stream)
         elif self._rows(batch, ("o", o, self.heads)):
             raise ValueError("o must be contiguous")
         if lse is None:
-            lse = torch.empty((batch.tokens, self.heads), dtype=torch.float32, device=self.device)
+            lse = _empty((batch.tokens, self.heads), torch.float32, self.device, stream)
         else:
             _plain("lse", lse, torch.float32, self.index, (batch.tokens, self.heads))
         arl2_paged_attend(self.handle, batch.struct, q, ld, mask_block, o, lse, _stream_of(self.index, stream))
@@ -750,7 +771,7 @@ class PagedKVLayer:
         self._weights_shape(batch, w)
         _plain("lse", lse, torch.float32, self.index, (batch.tokens, self.heads))
         if w_out is None:
-            w_out = torch.empty(w.shape, dtype=torch.float32, device=self.device)
+            w_out = _empty(w.shape, torch.float32, self.device, stream)
         else:
             _plain("w_out", w_out, torch.float32, self.index, w.shape)
         arl2_paged_weights(self.handle, batch.struct, q, ld, mask_block, lse, decay, w, w_out, w.shape[2],
@@ -765,9 +786,9 @@ class PagedKVLayer:
         if dst_pages.dim() != 2 or dst_pages.shape[0] != n:
             raise ValueError("dst_pages: expected [streams, pages]")
         _plain("dst_pages", dst_pages, torch.int32, self.index)
-        w_out = torch.empty(w.shape, dtype=torch.float32, device=self.device)
-        kept = torch.empty((n, self.kv_heads, budget), dtype=torch.int32, device=self.device)
-        kv_len = torch.empty((n,), dtype=torch.int32, device=self.device)
+        w_out = _empty(w.shape, torch.float32, self.device, stream)
+        kept = _empty((n, self.kv_heads, budget), torch.int32, self.device, stream)
+        kv_len = _empty((n,), torch.int32, self.device, stream)
         arl2_paged_evict(self.handle, batch.struct, w, w.shape[2], budget, sink, recent, dst_pages, dst_pages.shape[1],
                          w_out, kept, kv_len, _stream_of(self.index, stream))
         return kv_len, w_out, kept

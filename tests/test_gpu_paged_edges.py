@@ -143,3 +143,33 @@ def test_fading_records_streams_that_it_leaves_out(dtype, d):
     c.layer.weights(c.batch, q, lse, w, decay=0.5, w_out=out)
     assert c.layer.last_error() == ERR_PAGE
     assert (out[0] == 3).all() and torch.equal(out[1], want[1])
+
+
+# ------------------------------------------------------------------ an explicit stream
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("op", ["prep", "append", "attend", "weights", "evict"])
+def test_outputs_belong_to_the_stream_that_writes_them(op, raw):
+    """With stream=, what a call allocates is not memory that the current stream has still to write."""
+    c = Paged("bf16", 4, 2, 128, 16, [(20, 60), (1, 300)], 8, dst=[40, 40]).to_gpu()
+    q, k = c.randn(c.T, 4, 128).cuda(), c.randn(c.T, 2, 128).cuda()
+    w, dst = torch.rand(2, 2, 300, generator=c.g).cuda(), c.dst.cuda()
+    prep, pos = arl2.QKPrep([128]), torch.arange(c.T, dtype=torch.int32)[:, None].cuda()
+    lse = c.layer.attend(c.batch, q)[1]
+    call = {"prep": lambda **s: arl2.qk_norm_rope(prep, q, k, pos, **s),
+            "append": lambda **s: (c.layer.append(c.batch, k, k, q=q, prep=prep, pos=pos, **s),),
+            "attend": lambda **s: c.layer.attend(c.batch, q, **s),
+            "weights": lambda **s: (c.layer.weights(c.batch, q, lse, w, **s),),
+            "evict": lambda **s: c.layer.evict(c.batch, w, dst, budget=40, **s)}[op]
+    want = [x.clone() for x in call()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(DELAY)
+    for x in [torch.empty_like(x) for x in want]:  # freed, and yet to be written by the current stream
+        x.fill_(3)
+    del x
+    got = call(stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    for x, ref in zip(got, want):
+        assert torch.equal(x, ref)
+    assert c.layer.last_error() == 0
