@@ -224,6 +224,12 @@ __device__ __forceinline__ int visible_keys(const SeqView& v, const FastDiv& mas
   return lim < 0 ? 0 : lim > v.kv ? v.kv : int(lim);
 }
 
+// log sum exp of a row from its maximum (log2 units) and its sum, which is 0 where
+// the row sees no key, and NaN where its logits are.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Division of an attention launch.  Query rows of one (stream, key head) are
 // the pairs (token, head of the group), token-major; a tile holds `qt` tokens, a
 // block kTiles tiles.  Item (f, hk): f = b * n_qblk + block.  Its work is counted

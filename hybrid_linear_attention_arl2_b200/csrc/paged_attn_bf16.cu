@@ -425,7 +425,7 @@ __device__ __forceinline__ void join_own(const PagedAttnParams& p, const Seg& s,
     for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(acc[x] * inv);
     store_row32(static_cast<__nv_bfloat16*>(p.o) + orow * 128 + q * 32, o, sectors);
   }
-  if (p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  if (p.lse) p.lse[orow] = row_lse(M, L);
 }
 
 // Warpgroup t: tile t's rows, one a thread, 64 keys a step.
@@ -576,7 +576,7 @@ __device__ __forceinline__ void softmax_role(const PagedAttnParams& p, SegReader
         if (!whole)
           p.part_ml[prow] = make_float2(m, l);
         else if (p.lse)
-          p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          p.lse[orow] = row_lse(m, l);
       }
       if (!whole) {
         // The warp whose piece of these rows comes last joins them, in a dual segment;

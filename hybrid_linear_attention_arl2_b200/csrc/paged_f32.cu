@@ -163,7 +163,7 @@ __device__ __forceinline__ void join_block(const PagedAttnParams& p, const Paged
     if (lane == 0) {
       max_of[r] = m[i] == -INFINITY ? 0.f : m[i];
       inv_of[r] = l[i] > 0.f ? 1.f / l[i] : 0.f;
-      if (p.lse) p.lse[out(r)] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+      if (p.lse) p.lse[out(r)] = row_lse(m[i], l[i]);
     }
   }
   __syncthreads();
@@ -366,7 +366,7 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
         if (!whole)
           p.part_ml[int64_t(piece) * kRows + r] = make_float2(m[a], l[a]);
         else if (p.lse)
-          p.lse[orow] = l[a] > 0.f ? (m[a] + log2f(l[a])) * 0.69314718055994531f : -INFINITY;
+          p.lse[orow] = row_lse(m[a], l[a]);
       }
     }
     if (!whole) {

@@ -104,7 +104,7 @@ __device__ __forceinline__ void join_some(const PagedAttnParams& p, int owner, i
                make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
     }
   }
-  if (lane < n && p.lse) p.lse[out(r0 + lane)] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  if (lane < n && p.lse) p.lse[out(r0 + lane)] = row_lse(M, L);
 }
 
 // The same, with more pieces in flight where the rows are few: one token of 16

@@ -322,10 +322,11 @@ arl2_status arl2_paged_append(arl2_paged_t h, const arl2_paged_batch* batch, con
  *   q   : [tokens, H, head_dim], token rows ld_q elements apart (0: contiguous).
  *   o   : [tokens, H, head_dim] contiguous, shares no byte with q, lse or the pools.
  *   lse : float32 [tokens, H], log sum exp of a row's scaled logits; may be null.
- * A row that sees no key gets O = 0 and lse = -inf.  K and V of the
- * cached keys (those below kv_len) must be finite; what lies past kv_len in the
- * pool is not used, whatever it is.  A query pass that is not to be kept appends to scratch pages of its
- * own table, as the calls take the pages anew each time. */
+ * A row that sees no key gets O = 0 and lse = -inf; one whose query is no number
+ * gets NaN for both, and others are not touched by it.  K and V of the cached
+ * keys (those below kv_len) must be finite; what lies past kv_len in the pool is
+ * not used, whatever it is.  A query pass that is not to be kept appends to
+ * scratch pages of its own table, as the calls take the pages anew each time. */
 arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, const void* q, int64_t ld_q,
                               int32_t mask_block, void* o, float* lse, void* stream);
 

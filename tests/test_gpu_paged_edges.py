@@ -173,3 +173,25 @@ def test_outputs_belong_to_the_stream_that_writes_them(op, raw):
     for x, ref in zip(got, want):
         assert torch.equal(x, ref)
     assert c.layer.last_error() == 0
+
+
+# ------------------------------------------------------------------ queries that are no numbers
+@pytest.mark.parametrize("dtype,H,hk,d,seqs", [
+    ("bf16", 4, 2, 128, [(1, 9000), (300, 700), (3, 40), (70, 70)]),
+    ("bf16", 16, 1, 128, [(1, 20000), (30, 500)]),
+    ("f32", 4, 2, 64, [(1, 5000), (100, 300), (3, 40)])])
+def test_rows_that_are_no_numbers(dtype, H, hk, d, seqs):
+    """A query of NaN has outputs and a logarithm of NaN, not those of a row that sees no key; its neighbours keep
+    their bits, whole items and cut ones."""
+    c = Paged(dtype, H, hk, d, 16, seqs, 23).to_gpu()
+    q = c.randn(c.T, H, d).cuda()
+    o, lse = c.layer.attend(c.batch, q, mask_block=1)
+    bad = torch.zeros(c.T, H, dtype=torch.bool)
+    for t, h in ((0, 1), (c.T // 2, 0), (c.T // 2, H - 1), (c.T - 1, H // 2)):
+        bad[t, h] = True
+    bad = bad.cuda()
+    q2 = q.masked_fill(bad[..., None], float("nan"))
+    o2, lse2 = c.layer.attend(c.batch, q2, mask_block=1)
+    assert c.layer.last_error() == 0
+    assert o2[bad].isnan().all() and lse2[bad].isnan().all()
+    assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
