@@ -14,6 +14,7 @@ namespace arl2 {
 
 constexpr uint32_t kDevPage = 9;  // ARL2_ERR_PAGE as kernels record it
 constexpr int kPagedMaxGroup = 64;
+constexpr int kMaxUnits = 0x7fffffff - (1 << 14);  // of a launch's work division, sums stay in 32 bits
 
 // Division of numbers below 2^30 by a divisor known on the host: a product and a
 // shift.  With s = ceil(log2 d) - 2 and m = ceil(2^(32 + s) / d), m d - 2^(32 + s)
@@ -65,10 +66,10 @@ struct PagedAttnParams {
   float* lse;           // [tokens, H] or null
   int32_t heads, kv_heads, group, d;
   int32_t mask_block;
-  FastDiv mask, per_group, per_blk;  // by mask_block, group, n_qblk
+  FastDiv mask, per_group, per_blk;  // by mask_block, group, a block's tokens
   float scale_log2;     // softmax scale * log2(e)
-  // work division (see PagedPlan): tokens of a tile, blocks of query rows per stream at most
-  int32_t qt, n_qblk, min_cost;
+  // work division (see PagedPlan): tokens of a tile, cost of a range at least
+  int32_t qt, min_cost;
   float* part_o;        // [2 * grid][rows][d] pieces of items that several CTAs share
   float2* part_ml;      // [2 * grid][rows] their running max (log2 units) and sum
   uint32_t* joined;     // [grid][8] pieces of a CTA's cut item that are in (a count for each warp's rows); zero between launches
@@ -232,54 +233,54 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // Division of an attention launch.  Query rows of one (stream, key head) are
 // the pairs (token, head of the group), token-major; a tile holds `qt` tokens, a
-// block kTiles tiles.  Item (f, hk): f = b * n_qblk + block.  Its work is counted
-// in units: with two tiles one unit is one tile of kKeys keys against both; a
+// block kTiles tiles.  An item is a block of a stream and a key head.  Its work is
+// counted in units: with two tiles one unit is one tile of kKeys keys against both; a
 // block of one tile (single tokens) splits its keys between the two halves of
-// the CTA, so a unit is two key tiles.  Items lie in a row, f first and key heads
-// within it, and the CTAs take equal contiguous ranges of the cost, kItemCost +
-// units an item (its start, end and output take as long as that many units), so
-// that ragged batches are spread as evenly as one long stream.  An item
-// cut by a range's end is finished from the CTAs' pieces by the one that comes
-// last: a CTA has at most two, one at its range's begin (slot 0) and one at its
-// end (slot 1).  An item has at least one unit, so that rows which see no key get
-// their zeros.  A range costs min_cost at least.  (The launch bounds the units
-// below 2^31.)
+// the CTA, so a unit is two key tiles.  Items lie in a row, streams first, their
+// blocks and key heads within them, and the CTAs take equal contiguous ranges of
+// the cost, kItemCost + units an item (its start, end and output take as long as
+// that many units), so that ragged batches are spread as evenly as one long
+// stream.  An item cut by a range's end is finished from the CTAs' pieces by the
+// one that comes last: a CTA has at most two, one at its range's begin (slot 0) and
+// one at its end (slot 1).  An item has at least one unit, so that rows which see
+// no key get their zeros.  A range costs min_cost at least.  Only blocks that exist
+// are looked at, tokens / block + streams at most, so that neither the time nor the
+// launch's limit on units (kMaxUnits) depends on how far max_q is above the streams'
+// lengths.
 template <int kTiles, int kKeys, int kItemCost_>
 struct PagedPlan {
   static constexpr int kItemCost = kItemCost_;
   struct Block {
-    int row0, t0, n_tok;  // first token row, its token in the stream, tokens (0: no item)
+    int row0, t0, n_tok;  // first token row, its token in the stream, tokens
     int tiles;            // 1 or 2
     int units;            // per key head
     int n, kv;            // the stream's new tokens and cached keys
     __device__ SeqView view() const { return SeqView{0, n, kv}; }
   };
 
-  __device__ static Block block(const PagedAttnParams& p, int f, uint32_t* err) {
+  // Blocks of a stream's rows.
+  __device__ static int blocks(const PagedAttnParams& p, const SeqView& v) {
+    return v.n > 0 ? p.per_blk.div(v.n - 1) + 1 : 0;
+  }
+  // Block k of a stream's.
+  __device__ static Block block(const PagedAttnParams& p, const SeqView& v, int k) {
     Block r;
-    const int b = p.per_blk.div(f);
-    const SeqView v = load_seq(p.s, b, err);
-    r.t0 = (f - b * p.n_qblk) * p.qt * kTiles;
+    r.t0 = k * p.qt * kTiles;
     r.row0 = v.q0 + r.t0;
     r.n = v.n, r.kv = v.kv;
     r.n_tok = min(v.n - r.t0, p.qt * kTiles);
     r.tiles = kTiles == 2 && r.n_tok > p.qt ? 2 : 1;
-    r.units = 0;
-    if (r.n_tok <= 0) {
-      r.n_tok = 0;
-      return r;
-    }
     const int nk = (visible_keys(v, p.mask, r.t0 + r.n_tok - 1) + kKeys - 1) / kKeys;
     r.units = max(1, kTiles == 2 && r.tiles == 1 ? (nk + 1) >> 1 : nk);
     return r;
   }
 };
 
-// One segment of a CTA's walk: units [u0, u1) of item (f, hk).
+// One segment of a CTA's walk: units [u0, u1) of the item of block `blk` of stream b and key head hk.
 template <class Plan>
 struct PagedSeg {
   typename Plan::Block blk;
-  int f, hk, u0, u1;
+  int b, hk, u0, u1;
   // the item's pieces when it is cut: CTAs owner, owner + 1, ...; the owner's is in slot owner_slot, the others' in 0
   int owner, pieces, owner_slot;
   int slot;  // of this CTA's piece
@@ -299,73 +300,115 @@ struct PagedWalk {
     const int big = (each + 1) * more;
     return cost < big ? cost / (each + 1) : more + (cost - big) / each;
   }
-  __device__ static int cost_of(const typename Plan::Block& blk, int kv_heads) {
-    return blk.units > 0 ? (blk.units + Plan::kItemCost) * kv_heads : 0;
+
+  // The blocks of all streams in order, up to 32 at a time, a lane each: use(blk, b,
+  // cost), with cost 0 in a lane without one, until it returns true.  A lane holds
+  // one of 32 streams; where none of them has more than one block, its block too.
+  template <class Use>
+  __device__ static void visit(const PagedAttnParams& p, uint32_t* err, const Use& use) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int s0 = 0; s0 < p.s.n_seqs; s0 += 32) {
+      SeqView v{0, -1, 0};
+      if (s0 + lane < p.s.n_seqs) v = load_seq(p.s, s0 + lane, err);
+      const int nb = Plan::blocks(p, v);
+      if (!__any_sync(0xffffffffu, nb > 1)) {
+        const typename Plan::Block blk = Plan::block(p, v, 0);
+        if (use(blk, s0 + lane, nb ? (blk.units + Plan::kItemCost) * p.kv_heads : 0)) return;
+        continue;
+      }
+      int upto = nb;  // blocks of the lanes up to this one
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+      for (int x0 = 0; x0 < all; x0 += 32) {
+        const int x = x0 + lane;
+        int src = 0;  // the lane whose stream block x is of
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, src + o - 1) <= x) src += o;
+        const int k = x - __shfl_sync(0xffffffffu, upto - nb, src);
+        const SeqView u{__shfl_sync(0xffffffffu, v.q0, src), __shfl_sync(0xffffffffu, v.n, src),
+                        __shfl_sync(0xffffffffu, v.kv, src)};
+        const typename Plan::Block blk = Plan::block(p, u, k);
+        if (use(blk, s0 + src, x < all ? (blk.units + Plan::kItemCost) * p.kv_heads : 0)) return;
+      }
+    }
   }
 
-  // Finds the CTA's range; called by one warp.  Two passes over the blocks of
-  // rows: their total, then the one that holds the range's begin.
+  // Finds the CTA's range; called by one warp.  Two passes over the blocks: their
+  // total, then the one that holds the range's begin (of 32 blocks or fewer one).
   __device__ void find(const PagedAttnParams& p, int cta, int grid) {
-    const int lane = threadIdx.x & 31, F = p.s.n_seqs * p.n_qblk;
+    const int lane = threadIdx.x & 31;
+    unsigned mine = 0;
     typename Plan::Block blk;
-    blk.units = 0;
-    int total = 0, mine = 0;
-#pragma unroll 1
-    for (int f = lane; f < F; f += 32) {
-      blk = Plan::block(p, f, cta == 0 ? p.err : nullptr);
-      mine += cost_of(blk, p.kv_heads);
-    }
-    total = __reduce_add_sync(0xffffffffu, mine);
-    const int ctas = min((total + p.min_cost - 1) / p.min_cost, grid);
+    int b = 0, c = 0, batches = 0;
+    visit(p, cta == 0 ? p.err : nullptr, [&](const typename Plan::Block& blk_, int b_, int c_) {
+      blk = blk_, b = b_, c = c_, ++batches;
+      mine = min(mine + unsigned(c_), 0x7fffffffu);
+      return false;
+    });
+    const unsigned high = __reduce_add_sync(0xffffffffu, mine >> 8), low = __reduce_add_sync(0xffffffffu, mine & 255u);
     at = end = used = 0;
     have = fresh = true;
+    if (high > unsigned(kMaxUnits >> 8)) {  // (only rows that several streams claim come to so many)
+      if (cta == 0 && lane == 0) atomicCAS(p.err, 0u, kDevPage);
+      return;
+    }
+    const int total = int(high << 8) + int(low);
+    const int ctas = min((total + p.min_cost - 1) / p.min_cost, grid);
     if (cta >= ctas) return;
     each = total / ctas;
     more = total - each * ctas;
     const int pos = begin(cta);
     int before = 0;
-#pragma unroll 1
-    for (int f0 = 0; f0 < F; f0 += 32) {
-      if (F > 32) {
-        blk.units = 0;
-        if (f0 + lane < F) blk = Plan::block(p, f0 + lane, nullptr);
-      }
-      const int c = f0 + lane < F ? cost_of(blk, p.kv_heads) : 0;
-      int inc = c;
+    auto search = [&](const typename Plan::Block& blk_, int b_, int c_) {
+      int inc = c_;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
       }
-      const int off = pos - (before + inc - c);
-      const unsigned hit = __ballot_sync(0xffffffffu, off >= 0 && off < c);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const int in = __shfl_sync(0xffffffffu, off, src);
-        int* w = reinterpret_cast<int*>(&blk);
-        for (int i = 0; i < int(sizeof(blk) / 4); ++i) w[i] = __shfl_sync(0xffffffffu, w[i], src);
-        seg.blk = blk;
-        seg.f = f0 + src;
-        seg.hk = in / (blk.units + Plan::kItemCost);
-        const int inner = in - seg.hk * (blk.units + Plan::kItemCost);
-        at = pos - inner;
-        seg.u1 = max(0, inner - Plan::kItemCost);  // (the next segment begins at u1)
-        end = begin(cta + 1);
-        return;
-      }
+      const int off = pos - (before + inc - c_);
+      const unsigned hit = __ballot_sync(0xffffffffu, off >= 0 && off < c_);
       before += __shfl_sync(0xffffffffu, inc, 31);
-    }
+      if (!hit) return false;
+      const int src = __ffs(hit) - 1;
+      const int in = __shfl_sync(0xffffffffu, off, src);
+      typename Plan::Block found = blk_;
+      int* w = reinterpret_cast<int*>(&found);
+      for (int i = 0; i < int(sizeof(found) / 4); ++i) w[i] = __shfl_sync(0xffffffffu, w[i], src);
+      seg.blk = found;
+      seg.b = __shfl_sync(0xffffffffu, b_, src);
+      seg.hk = in / (found.units + Plan::kItemCost);
+      const int inner = in - seg.hk * (found.units + Plan::kItemCost);
+      at = pos - inner;
+      seg.u1 = max(0, inner - Plan::kItemCost);  // (the next segment begins at u1)
+      end = begin(cta + 1);
+      return true;
+    };
+    if (batches == 1)
+      search(blk, b, c);
+    else
+      visit(p, nullptr, search);
   }
 
   // The next segment with units; a range may end or begin in an item's kItemCost.
   __device__ bool next(const PagedAttnParams& p) {
     while (at < end) {
       if (!have) {
-        const int F = p.s.n_seqs * p.n_qblk;
-        do {
-          if (++seg.f >= F) return false;  // (cannot happen: the range lies inside the items)
-          seg.blk = Plan::block(p, seg.f, nullptr);
-        } while (seg.blk.units == 0);
+        SeqView v{seg.blk.row0 - seg.blk.t0, seg.blk.n, seg.blk.kv};
+        int k = p.per_blk.div(seg.blk.t0) + 1;
+        while (k >= Plan::blocks(p, v)) {
+          if (++seg.b >= p.s.n_seqs) return false;  // (cannot happen: the range lies inside the items)
+          v = load_seq(p.s, seg.b, nullptr);
+          k = 0;
+        }
+        seg.blk = Plan::block(p, v, k);
         seg.hk = 0;
         have = true;
       }
@@ -406,18 +449,18 @@ struct PagedWalk {
 };
 #endif  // __CUDACC__
 
-// Host side of the division: fills p's tile and block counts; false where the
-// units would not fit 31 bits.
+// Host side of the division: fills p's tile; false where the units could pass
+// kMaxUnits.  A stream of n tokens has n / block + 1 blocks at most.
 inline bool paged_plan(PagedAttnParams& p, int tile_rows, int tiles, int keys) {
   p.qt = tile_rows / p.group;
-  const int64_t tokens = int64_t(p.qt) * tiles;
-  const int64_t n_qblk = (p.s.max_q + tokens - 1) / tokens;
-  if (n_qblk * p.s.n_seqs >= (int64_t(1) << 30)) return false;
-  if (double(n_qblk) * p.s.n_seqs * (p.s.max_kv / keys + 8) * p.kv_heads >= 2147483647.0) return false;
-  p.n_qblk = int32_t(n_qblk);
+  const int block = p.qt * tiles;
+  const double by_streams = double((int64_t(p.s.max_q) + block - 1) / block) * p.s.n_seqs;
+  const double by_tokens = double(p.s.tokens / block) + p.s.n_seqs;
+  const double blocks = by_streams < by_tokens ? by_streams : by_tokens;
+  if (blocks * (p.s.max_kv / keys + 8) * p.kv_heads >= double(kMaxUnits)) return false;
   p.mask = FastDiv(p.mask_block);
   p.per_group = FastDiv(p.group);
-  p.per_blk = FastDiv(p.n_qblk);
+  p.per_blk = FastDiv(block);
   return true;
 }
 

@@ -83,7 +83,7 @@ __device__ __forceinline__ void describe(Seg& g, const PagedSeg<Plan>& s, int ro
   const int qt = p.qt;
   g.more = 1;
   g.last = 0;
-  g.b = p.per_blk.div(s.f), g.hk = s.hk;
+  g.b = s.b, g.hk = s.hk;
   g.row0 = s.blk.row0;
   g.tok0 = s.blk.t0;
   g.n_new = s.blk.n, g.kv = s.blk.kv;

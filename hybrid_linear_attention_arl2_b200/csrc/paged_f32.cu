@@ -244,7 +244,7 @@ paged_attn_f32_kernel(const PagedAttnParams p) {
   const float* q = static_cast<const float*>(p.q);
   while (more) {
     const PagedSeg<Plan> s = walk.seg;
-    const int rows = s.blk.n_tok * p.group, b = p.per_blk.div(s.f);
+    const int rows = s.blk.n_tok * p.group, b = s.b;
     const float* k_pool = static_cast<const float*>(p.k_pool);
     const float* v_pool = static_cast<const float*>(p.v_pool);
     // the first keys' pages, query rows, and each of this thread's rows' visible keys

@@ -269,6 +269,9 @@ arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t h
  *             past the last page are not read).
  * The host gives bounds that size the launches: tokens (rows of the new-token
  * tensors), max_q and max_kv (at least any stream's new tokens and kv_len).
+ * They may be loose: attend counts its work in 32 bits, which always suffice
+ * where (tokens * heads / 32 + n_seqs * kv_heads) * (max_kv / 64 + 8) is below
+ * 2^31 - 2^14, whatever max_q is, and answers UNSUPPORTED where they might not.
  * What the kernels find out of range they do not access: a stream whose rows
  * or lengths break a bound is left out (its outputs stay as they were, but for
  * arl2_paged_evict's), a page number outside [0, n_pages) reads as zeros and is

@@ -195,3 +195,53 @@ def test_rows_that_are_no_numbers(dtype, H, hk, d, seqs):
     assert c.layer.last_error() == 0
     assert o2[bad].isnan().all() and lse2[bad].isnan().all()
     assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
+
+
+# ------------------------------------------------------------------ bounds far above the work
+MIXED = [  # dtype, heads, kv_heads, d, chunk, its keys, streams of one token
+    ("bf16", 8, 1, 128, 1500, 1700, 200),
+    ("f32", 8, 2, 32, 700, 900, 150),
+]
+
+
+def check_rows(c, q, o, lse, mask, rows):
+    used = c.tables[c.tables >= 0].long()
+    kp, vp = np.nan_to_num(host(c.kp)), np.nan_to_num(host(c.vp))
+    ref, ref_l, mag = po.attend(host(q)[:c.T], kp, vp, c.seqs, c.tables.numpy(), mask, rows=set(rows.tolist()))
+    bo, bl = attend_bounds(c.dtype, c.d, host(q)[:c.T], kp[used.numpy()].reshape(-1, c.d), c.width, mag, ref)
+    assert (np.abs(host(o)[:c.T] - ref) <= bo)[rows].all() and (np.abs(host(lse)[:c.T] - ref_l) <= bl)[rows].all()
+
+
+@pytest.mark.parametrize("dtype,H,hk,d,chunk,keys,tokens", MIXED)
+@pytest.mark.parametrize("place", ["first", "last", "between"])
+def test_single_tokens_beside_a_chunk(dtype, H, hk, d, chunk, keys, tokens, place):
+    """Many streams of one token, some of none, beside one of many blocks of rows: attention, and the weights' sums."""
+    seqs = [(1 if i % 7 else 0, 1 + (37 * i) % 90) for i in range(tokens)]
+    seqs.insert({"first": 0, "last": tokens, "between": tokens // 3}[place], (chunk, keys))
+    c = Paged(dtype, H, hk, d, 16, seqs, 29).to_gpu()
+    q = c.randn(c.T, H, d).cuda()
+    o, lse = c.layer.attend(c.batch, q, mask_block=1)
+    at = sum(n for n, _ in seqs[:seqs.index((chunk, keys))])
+    rows = np.unique(np.clip(np.r_[0:c.T:11, at - 2:at + 40, at + chunk - 40:at + chunk + 3, at + 250:at + 262], 0, c.T - 1))
+    check_rows(c, q, o, lse, 1, rows)
+    w = c.layer.weights(c.batch, q, lse, torch.zeros(len(seqs), hk, c.width, device="cuda"), mask_block=1)
+    # each row of a key head hands out weight one, up to its lse's rounding and the sums'
+    want = torch.tensor([float(n * (H // hk)) for n, _ in seqs])[:, None].expand(-1, hk)
+    assert torch.allclose(w.sum(-1).cpu(), want, rtol=1e-4)
+    assert c.layer.last_error() == 0
+
+
+@pytest.mark.parametrize("dtype,H,hk,d", [("bf16", 64, 8, 128), ("f32", 64, 8, 16)])
+def test_bounds_far_above_the_work(dtype, H, hk, d):
+    """1024 streams of at most a few tokens, with bounds that would allow each 8192 on 131072 keys (2^31 tiles of keys
+    and more in all): what a graph for chunks meets when it replays single tokens."""
+    seqs = [(1 + (i % 97 == 5) * 2, 3 + i % 29) for i in range(1024)]
+    c = Paged(dtype, H, hk, d, 16, seqs, 31).to_gpu(max_q=8192, max_kv=131072)
+    q = c.randn(c.T, H, d).cuda()
+    o, lse = c.layer.attend(c.batch, q, mask_block=1)
+    rows = np.r_[0:12, 500:520, c.T - 9:c.T]
+    check_rows(c, q, o, lse, 1, rows)
+    tight = arl2.PagedBatch(c.batch.q_start, c.batch.kv_len, c.batch.pages, tokens=c.T, max_q=3, max_kv=c.width)
+    o2, lse2 = c.layer.attend(tight, q, mask_block=1)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)  # (no stream is long enough for its tiles to be cut)
+    assert c.layer.last_error() == 0
