@@ -14,7 +14,7 @@ namespace arl2 {
 
 constexpr uint32_t kDevPage = 9;  // ARL2_ERR_PAGE as kernels record it
 constexpr int kPagedMaxGroup = 64;
-constexpr int kMaxUnits = 0x7fffffff - (1 << 14);  // of a launch's work division, sums stay in 32 bits
+constexpr int kMaxUnits = 0x7fffffff - (1 << 14);  // of a launch's work division: sums stay in 32 bits
 
 // Division of numbers below 2^30 by a divisor known on the host: a product and a
 // shift.  With s = ceil(log2 d) - 2 and m = ceil(2^(32 + s) / d), m d - 2^(32 + s)
@@ -184,10 +184,9 @@ struct SeqView {
   int q0, n, kv;  // first row, new tokens, cached keys
 };
 
-// Stream b, or n = -1 when its rows or lengths break the batch's bounds (it is
-// then left out by every kernel; the error is recorded).
-__device__ __forceinline__ SeqView load_seq(const PagedSeqs& s, int b, uint32_t* err) {
-  const int q0 = s.q_start[b], q1 = s.q_start[b + 1], kv = s.kv_len[b];
+// A stream of rows [q0, q1) and kv keys, n = -1 when they break the batch's bounds
+// (it is then left out by every kernel; the error is recorded).
+__device__ __forceinline__ SeqView checked_seq(const PagedSeqs& s, int q0, int q1, int kv, uint32_t* err) {
   SeqView v{q0, q1 - q0, kv};
   if (q0 < 0 || q1 < q0 || q1 > s.tokens || q1 - q0 > s.max_q || kv < 0 || kv > s.max_kv ||
       kv > int64_t(s.pages_ld) * s.page_size) {
@@ -195,6 +194,10 @@ __device__ __forceinline__ SeqView load_seq(const PagedSeqs& s, int b, uint32_t*
     v = SeqView{0, -1, 0};
   }
   return v;
+}
+
+__device__ __forceinline__ SeqView load_seq(const PagedSeqs& s, int b, uint32_t* err) {
+  return checked_seq(s, s.q_start[b], s.q_start[b + 1], s.kv_len[b], err);
 }
 
 // As load_seq for the calls that use a stream's cache alone.
@@ -276,6 +279,14 @@ struct PagedPlan {
   }
 };
 
+// The sum of the lanes' units, each below 2^31; false where it is above kMaxUnits,
+// as it can only be of rows that several streams claim.
+__device__ __forceinline__ bool sum_units(unsigned mine, int& total) {
+  const unsigned high = __reduce_add_sync(0xffffffffu, mine >> 8), low = __reduce_add_sync(0xffffffffu, mine & 255u);
+  total = int(high << 8) + int(low);
+  return high <= unsigned(kMaxUnits >> 8);
+}
+
 // One segment of a CTA's walk: units [u0, u1) of the item of block `blk` of stream b and key head hk.
 template <class Plan>
 struct PagedSeg {
@@ -307,35 +318,45 @@ struct PagedWalk {
   template <class Use>
   __device__ static void visit(const PagedAttnParams& p, uint32_t* err, const Use& use) {
     const int lane = threadIdx.x & 31;
+    int q0 = 0, q1 = 0, kv = 0;  // (a lane without a stream has one without tokens)
+    auto fetch = [&](int b) {
+      q0 = q1 = kv = 0;
+      if (b < p.s.n_seqs) q0 = p.s.q_start[b], q1 = p.s.q_start[b + 1], kv = p.s.kv_len[b];
+    };
+    fetch(lane);
 #pragma unroll 1
     for (int s0 = 0; s0 < p.s.n_seqs; s0 += 32) {
-      SeqView v{0, -1, 0};
-      if (s0 + lane < p.s.n_seqs) v = load_seq(p.s, s0 + lane, err);
+      const SeqView v = checked_seq(p.s, q0, q1, kv, err);
+      fetch(s0 + 32 + lane);
       const int nb = Plan::blocks(p, v);
-      if (!__any_sync(0xffffffffu, nb > 1)) {
-        const typename Plan::Block blk = Plan::block(p, v, 0);
-        if (use(blk, s0 + lane, nb ? (blk.units + Plan::kItemCost) * p.kv_heads : 0)) return;
-        continue;
-      }
-      int upto = nb;  // blocks of the lanes up to this one
+      const bool shared = __any_sync(0xffffffffu, nb > 1);
+      int upto = nb, all = 32;  // blocks of the lanes up to this one, and of all
+      if (shared) {
 #pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        all = __shfl_sync(0xffffffffu, upto, 31);
       }
-      const int all = __shfl_sync(0xffffffffu, upto, 31);
 #pragma unroll 1
       for (int x0 = 0; x0 < all; x0 += 32) {
-        const int x = x0 + lane;
-        int src = 0;  // the lane whose stream block x is of
+        SeqView u = v;
+        int k = 0, src = lane;
+        bool some = nb > 0;
+        if (shared) {
+          const int x = x0 + lane;
+          some = x < all;
+          src = 0;  // the lane whose stream block x is of
 #pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1)
-          if (__shfl_sync(0xffffffffu, upto, src + o - 1) <= x) src += o;
-        const int k = x - __shfl_sync(0xffffffffu, upto - nb, src);
-        const SeqView u{__shfl_sync(0xffffffffu, v.q0, src), __shfl_sync(0xffffffffu, v.n, src),
-                        __shfl_sync(0xffffffffu, v.kv, src)};
+          for (int o = 16; o > 0; o >>= 1)
+            if (__shfl_sync(0xffffffffu, upto, src + o - 1) <= x) src += o;
+          k = x - __shfl_sync(0xffffffffu, upto - nb, src);
+          u = SeqView{__shfl_sync(0xffffffffu, v.q0, src), __shfl_sync(0xffffffffu, v.n, src),
+                      __shfl_sync(0xffffffffu, v.kv, src)};
+        }
         const typename Plan::Block blk = Plan::block(p, u, k);
-        if (use(blk, s0 + src, x < all ? (blk.units + Plan::kItemCost) * p.kv_heads : 0)) return;
+        if (use(blk, s0 + src, some ? (blk.units + Plan::kItemCost) * p.kv_heads : 0)) return;
       }
     }
   }
@@ -352,14 +373,13 @@ struct PagedWalk {
       mine = min(mine + unsigned(c_), 0x7fffffffu);
       return false;
     });
-    const unsigned high = __reduce_add_sync(0xffffffffu, mine >> 8), low = __reduce_add_sync(0xffffffffu, mine & 255u);
     at = end = used = 0;
     have = fresh = true;
-    if (high > unsigned(kMaxUnits >> 8)) {  // (only rows that several streams claim come to so many)
+    int total;
+    if (!sum_units(mine, total)) {
       if (cta == 0 && lane == 0) atomicCAS(p.err, 0u, kDevPage);
       return;
     }
-    const int total = int(high << 8) + int(low);
     const int ctas = min((total + p.min_cost - 1) / p.min_cost, grid);
     if (cta >= ctas) return;
     each = total / ctas;
@@ -449,15 +469,18 @@ struct PagedWalk {
 };
 #endif  // __CUDACC__
 
-// Host side of the division: fills p's tile; false where the units could pass
-// kMaxUnits.  A stream of n tokens has n / block + 1 blocks at most.
+// Host side: blocks of `block` tokens at most in a batch's streams (one of n tokens
+// has n / block + 1 at most).
+inline double most_blocks(const PagedSeqs& s, int block) {
+  const double by_streams = double(s.max_q / block + 1) * s.n_seqs, by_tokens = double(s.tokens / block) + s.n_seqs;
+  return by_streams < by_tokens ? by_streams : by_tokens;
+}
+
+// Of the division: fills p's tile; false where the units could pass kMaxUnits.
 inline bool paged_plan(PagedAttnParams& p, int tile_rows, int tiles, int keys) {
   p.qt = tile_rows / p.group;
   const int block = p.qt * tiles;
-  const double by_streams = double((int64_t(p.s.max_q) + block - 1) / block) * p.s.n_seqs;
-  const double by_tokens = double(p.s.tokens / block) + p.s.n_seqs;
-  const double blocks = by_streams < by_tokens ? by_streams : by_tokens;
-  if (blocks * (p.s.max_kv / keys + 8) * p.kv_heads >= double(kMaxUnits)) return false;
+  if (most_blocks(p.s, block) * (p.s.max_kv / keys + 8) * p.kv_heads >= double(kMaxUnits)) return false;
   p.mask = FastDiv(p.mask_block);
   p.per_group = FastDiv(p.group);
   p.per_blk = FastDiv(block);
