@@ -510,7 +510,7 @@ arl2_status arl2_paged_weights(arl2_paged_t h, const arl2_paged_batch* batch, co
   p.per_group = FastDiv(p.group);
   const int keys = c.dtype == ARL2_BF16 ? 256 : 64;
   p.per_tile = FastDiv((c.dtype == ARL2_BF16 ? 128 : 64) / p.group);
-  if (double(batch->n_seqs) * c.kv_heads * (batch->max_kv / keys + 1) * (batch->max_q / p.per_tile.by + 1) >= 2147483647.0)
+  if (most_blocks(p.s, p.per_tile.by) * (batch->max_kv / keys + 1) * c.kv_heads >= double(kMaxUnits))
     return ARL2_ERR_UNSUPPORTED;
   p.part_w = h->part_o;
   p.joined = h->joined;

@@ -269,9 +269,9 @@ arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t h
  *             past the last page are not read).
  * The host gives bounds that size the launches: tokens (rows of the new-token
  * tensors), max_q and max_kv (at least any stream's new tokens and kv_len).
- * They may be loose: attend counts its work in 32 bits, which always suffice
+ * They may be loose: attend and weights count work in 32 bits, which always suffice
  * where (tokens * heads / 32 + n_seqs * kv_heads) * (max_kv / 64 + 8) is below
- * 2^31 - 2^14, whatever max_q is, and answers UNSUPPORTED where they might not.
+ * 2^31 - 2^14, whatever max_q is, and answer UNSUPPORTED where they might not.
  * What the kernels find out of range they do not access: a stream whose rows
  * or lengths break a bound is left out (its outputs stay as they were, but for
  * arl2_paged_evict's), a page number outside [0, n_pages) reads as zeros and is
@@ -372,8 +372,8 @@ arl2_status arl2_paged_evict(arl2_paged_t h, const arl2_paged_batch* batch, cons
 /* Wait for the handle's device, whatever streams its calls and the replays of
  * captured ones ran on, and return (and clear) the first error recorded by its
  * kernels (ARL2_ERR_PAGE, ARL2_ERR_TIMEOUT), ARL2_OK if none.  After
- * ARL2_ERR_TIMEOUT a call's outputs are undefined, and so are those of later
- * calls until this one has returned. */
+ * ARL2_ERR_TIMEOUT, or a q_start that decreases, a call's outputs are undefined,
+ * and so are those of later calls until this one has returned. */
 arl2_status arl2_paged_last_error(arl2_paged_t h);
 int64_t arl2_paged_device_bytes(arl2_paged_t h);
 /* As arl2_state_set_wait_limit. */

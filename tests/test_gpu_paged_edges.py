@@ -245,3 +245,20 @@ def test_bounds_far_above_the_work(dtype, H, hk, d):
     o2, lse2 = c.layer.attend(tight, q, mask_block=1)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)  # (no stream is long enough for its tiles to be cut)
     assert c.layer.last_error() == 0
+
+
+@pytest.mark.parametrize("dtype,H,hk,d", [("bf16", 64, 8, 128), ("f32", 64, 8, 16)])
+def test_weights_with_bounds_far_above_the_work(dtype, H, hk, d):
+    """The weights of such a batch, whose bounds' product is past 2^31 units."""
+    seqs = [(1 + (i % 97 == 5) * 2, 3 + i % 29) for i in range(256)]
+    c = Paged(dtype, H, hk, d, 16, seqs, 33).to_gpu(max_q=1 << 20, max_kv=4096)
+    q = c.randn(c.T, H, d).cuda()
+    tight = arl2.PagedBatch(c.batch.q_start, c.batch.kv_len, c.batch.pages, tokens=c.T, max_q=3, max_kv=c.width)
+    lse = c.layer.attend(tight, q, mask_block=1)[1]
+    w = torch.rand(len(seqs), hk, 4096, generator=c.g).cuda()
+    got = c.layer.weights(c.batch, q, lse, w, mask_block=1, decay=0.5)
+    ref = c.layer.weights(tight, q, lse, w, mask_block=1, decay=0.5)
+    assert torch.equal(got, ref) and c.layer.last_error() == 0
+    want = torch.tensor([float(n * (H // hk)) for n, _ in seqs])[:, None].expand(-1, hk)
+    faded = torch.stack([0.5 * w[b, :, :kv].sum(-1) for b, (_, kv) in enumerate(seqs)]).cpu()
+    assert torch.allclose(got.sum(-1).cpu() - faded, want, rtol=1e-3)
