@@ -262,3 +262,49 @@ def test_weights_with_bounds_far_above_the_work(dtype, H, hk, d):
     want = torch.tensor([float(n * (H // hk)) for n, _ in seqs])[:, None].expand(-1, hk)
     faded = torch.stack([0.5 * w[b, :, :kv].sum(-1) for b, (_, kv) in enumerate(seqs)]).cpu()
     assert torch.allclose(got.sum(-1).cpu() - faded, want, rtol=1e-3)
+
+
+# ------------------------------------------------------------------ runs
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 32)])
+def test_a_stream_stays_at_its_budget(dtype, d):
+    """Chunk after chunk through append, attention, weights and eviction: the lengths grow to the budget and stay."""
+    H, hk, page, budget, chunk = 4, 2, 16, 48, 20
+    c = Paged(dtype, H, hk, d, page, [(chunk, chunk), (chunk, chunk)], 8, spare=20).to_gpu(max_kv=budget + chunk)
+    each = -(-(budget + chunk) // page)
+    tables = [torch.arange(i * 2 * each, (i + 1) * 2 * each, dtype=torch.int32).view(2, each).cuda() for i in range(2)]
+    kv, w = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, hk, budget + chunk, device="cuda")
+    for rnd in range(6):
+        kv += chunk
+        batch = arl2.PagedBatch(c.batch.q_start, kv, tables[rnd % 2], tokens=2 * chunk, max_q=chunk, max_kv=budget + chunk)
+        k, v, q = c.randn(2 * chunk, hk, d).cuda(), c.randn(2 * chunk, hk, d).cuda(), c.randn(2 * chunk, H, d).cuda()
+        c.layer.append(batch, k, v)
+        w = c.layer.weights(batch, q, c.layer.attend(batch, q, mask_block=1)[1], w, mask_block=1)
+        kv, w, kept = c.layer.evict(batch, w, tables[(rnd + 1) % 2], budget=budget, sink=2, recent=8)
+        n = min(budget, (rnd + 1) * chunk)
+        assert kv.tolist() == [n, n]
+        assert (kept[:, :, :n] >= 0).all() and (kept[:, :, n:] == -1).all()
+        assert (kept[:, :, 1:n] > kept[:, :, :n - 1]).all()
+    assert c.layer.last_error() == 0
+
+
+def test_norm_and_rotation_before_a_hybrid_layer():
+    """A fused row turned in place, then read by the hybrid layer through its pitch: what a block with head norms and
+    positions does.  Equal to turned copies, contiguous, bit by bit."""
+    from hybrid_linear_attention_arl2_b200 import workloads as W
+    from tests.gpu_util import make_layer, small_config
+    cfg = small_config(B=2, H=3, L=200)
+    layer, _ = make_layer(cfg, W.Workload(cfg))
+    B, L, H, d = cfg.batch, cfg.tokens, cfg.heads, 128
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randn(B * L, 3 * H * d, generator=g).to(torch.bfloat16).cuda()
+    w_q, w_k = ((1 + 0.1 * torch.randn(d, generator=g)).to(torch.bfloat16).cuda() for _ in range(2))
+    pos = torch.stack([torch.arange(B * L) // L, torch.arange(B * L) % L // 20, torch.arange(B * L) % 20], 1).int().cuda()
+    prep = arl2.QKPrep([44, 42, 42], w_q=w_q, w_k=w_k)
+    q, k, v = (rows[:, i * H * d:(i + 1) * H * d].unflatten(1, (H, d)) for i in range(3))
+    turned = arl2.qk_norm_rope(prep, q, k, pos)
+    ref = layer.query(*(x.contiguous().view(B, L, H, d) for x in (*turned, v)))
+    arl2.qk_norm_rope(prep, q, k, pos, q_out=q, k_out=k)
+    o = torch.empty_like(ref)
+    arl2.arl2_frame_query_strided(layer.handle, q, k, v, rows.shape[1], o)
+    assert layer.last_error() == 0 and torch.equal(o, ref)
+    layer.close()
