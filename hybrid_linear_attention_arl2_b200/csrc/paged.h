@@ -163,7 +163,7 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 cudaError_t launch_prep(const PrepParams& p, int dtype, bool append, int sms, cudaStream_t st);
 // Attention: CTAs of the launch and rows of one of their pieces at most, which
 // size the handle's work space; then the launches.
-// (float32: two blocks to an SM with head dims up to 64)
+// (float32: two blocks to an SM)
 inline int paged_attn_grid(int dtype, int sms) { return dtype == ARL2_BF16 ? sms : 2 * sms; }
 inline int paged_piece_rows(int dtype) { return dtype == ARL2_BF16 ? 256 : 64; }
 cudaError_t launch_paged_attn_f32(PagedAttnParams p, int grid, cudaStream_t st);

@@ -16,7 +16,9 @@
 // for two CTAs an SM with 128 columns, and one's products pass while the other
 // waits.  1000 causal tokens of 4 heads of 128 columns on 5000 keys: 320 us, 29
 // TFLOP/s (541 with tiles loaded between barriers, one CTA an SM); single tokens
-// of 16 heads on 2 key heads over 29300 keys: 103 us (154).
+// of 16 heads on 2 key heads over 29300 keys: 93 us (154).  Neither pipe is full:
+// shared memory moves in 58 % of the clocks, without conflicts, and an instruction
+// issues in 49 %; 16 warps an SM do not hide the two barriers a tile.
 
 #include <cuda_bf16.h>
 

@@ -311,7 +311,9 @@ arl2_status arl2_paged_init(const arl2_paged_config* cfg, void* k_pool, void* v_
  *           contiguous); q and q_out may both be null.  pos: int32 [tokens, n_axes].
  *   q_out : [tokens, H, head_dim] contiguous; may be q itself when q is
  *           contiguous, and otherwise shares no byte with an input.
- * Tokens before key 0 (kv_len < n) are ARL2_ERR_PAGE and not stored. */
+ * Tokens before key 0 (kv_len < n) are ARL2_ERR_PAGE and not stored.  Streams may
+ * share the pages that they read (a common prefix); a row that is stored to must
+ * be one stream's. */
 arl2_status arl2_paged_append(arl2_paged_t h, const arl2_paged_batch* batch, const arl2_qk_prep* prep, const void* q,
                               const void* k, const void* v, int64_t ld, const int32_t* pos, void* q_out,
                               void* stream);
@@ -338,7 +340,7 @@ arl2_status arl2_paged_attend(arl2_paged_t h, const arl2_paged_batch* batch, con
  * decayed sum so far:
  *   w_out[b][hk][j] = decay * w_in[b][hk][j] + sum exp(q k_j * scale - lse[row])
  * over the rows that see key j.  lse is arl2_paged_attend's for the same
- * batch, q and mask_block (rows with lse = -inf add nothing).  w_in, w_out:
+ * batch, q and mask_block (rows with lse = -inf, and finite q, add nothing).  w_in, w_out:
  * float32 [n_seqs, Hk, w_ld], w_ld >= max_kv; w_out may be w_in (equal pointer)
  * and otherwise shares no byte with it.  Entries from kv_len on are set to 0
  * in w_out (not read in w_in), so that tokens appended later start from 0. */
