@@ -275,7 +275,9 @@ arl2_status arl2_qk_norm_rope(const arl2_qk_prep* prep, int32_t dtype, int32_t h
  * What the kernels find out of range they do not access: a stream whose rows
  * or lengths break a bound is left out (its outputs stay as they were, but for
  * arl2_paged_evict's), a page number outside [0, n_pages) reads as zeros and is
- * not written; both record ARL2_ERR_PAGE for arl2_paged_last_error. */
+ * not written; both record ARL2_ERR_PAGE for arl2_paged_last_error.  (Calls that
+ * launch nothing record nothing: append and attend with tokens = 0, attend with
+ * max_q = 0.) */
 typedef struct {
   int32_t heads;        /* H query heads */
   int32_t kv_heads;     /* Hk: divides heads; heads / kv_heads <= 64 */
